@@ -416,6 +416,159 @@ mtp_status mtp_paged_decode_attn(const uint16_t* q, int32_t nq, int32_t nkv, int
                                  size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * The block-scaled paged cache: E4M3 K and V in blocks of `block_size` tokens with one fp32
+ * scale for each block and kv head, so that the codes' range follows the data. The pages
+ * have one scale per tensor ([new.rs]: an FP8 cache fed unit K/V scales) and no formulas for
+ * what follows; these entry points serve a batch of sequences, several tokens each.
+ *
+ * mtp_block_cache describes the cache (host struct; device pointers inside). Code d of head
+ * g, row r of block n is k[n * block_stride + g * head_stride + r * row_stride + d] (strides
+ * in bytes, the same for v), so both [block, head, row, hd] (one block's rows of one head
+ * contiguous: the faster one to read) and mtp_prefill_kv's [block, row, head, hd] are
+ * described; a cache that mtp_prefill_kv wrote is read with scales all equal to its k_scale
+ * and v_scale. dequant = e4m3(code) * scale[n * nkv + g]; a scale is a finite number >= 0.
+ * k_mean and k_mean_scale (both or neither) hold each block's mean key per head:
+ * mean = k_mean[(n * nkv + g) * hd + d] * k_mean_scale[n * nkv + g].
+ *
+ * Shared arguments and rules of the five entry points:
+ *   seq_lens    (device) i32 [B]: positions of sequence b after this step's tokens (the same
+ *               number for the append and the attention of one step); negative reads as 0
+ *   q_lens      (device) i32 [B] or NULL (= T): how many of sequence b's T token slots hold a
+ *               token; the others are padding, their outputs are left as they were. Clamped
+ *               to [0, T]
+ *   block_table (device) i32 [B, n_table]: physical block of each logical one. Position p of
+ *               sequence b is row p % block_size of block block_table[b, p / block_size]
+ *   Token t of sequence b is position seq_len - q_len + t and sees the positions
+ *   p < lim(b, t) = seq_len - q_len + t + 1. A position whose block is missing (logical
+ *   block >= n_table, physical one outside [0, num_blocks)) is skipped and sets
+ *   MTP_DEVFLAG_BAD_SLOT in dev_err (device i32 [1] or NULL).
+ * Requires hd in {64, 128, 256}, block_size in {16, 32, 64}, 1 <= B <= 65535, nkv <= 4096,
+ * num_blocks < 2^31, n_table * block_size <= 2^30 (MTP_ERR_UNSUPPORTED otherwise); codes, means and bf16 tensors 16-byte
+ * aligned, cache strides positive multiples of 16 bytes with row_stride >= hd, bf16 token
+ * strides multiples of 8 elements. Rows of different sequences may share blocks that are only read.
+ * ------------------------------------------------------------------------------ */
+typedef struct {
+    int32_t nkv;
+    int32_t hd;
+    int32_t block_size;
+    int32_t reserved; /* must be 0 */
+    int64_t num_blocks;
+    int64_t block_stride; /* bytes between blocks */
+    int64_t head_stride;  /* bytes between a block's heads */
+    int64_t row_stride;   /* bytes between a head's rows in a block */
+    uint8_t* k;           /* E4M3 codes */
+    uint8_t* v;
+    float* k_scale;       /* f32 [num_blocks, nkv] */
+    float* v_scale;
+    int8_t* k_mean;       /* i8 [num_blocks, nkv, hd] or NULL */
+    float* k_mean_scale;  /* f32 [num_blocks, nkv] or NULL */
+} mtp_block_cache;
+
+/* mtp_block_append -- writes each sequence's new K and V rows into its blocks, and brings the
+ * scales and means of the blocks they fall in up to date.
+ * For a block and head with new rows x (fp32 from bf16) and `old` rows of the sequence before
+ * them in the block:
+ *   a = the largest finite |x|;  s_new = the least power of two >= a / 448 (0 if a = 0; kept
+ *   within [2^-110, 2^120]);  s = max(s_new, the block's scale if it has old rows)
+ *   new codes = e4m3_satfinite(x / s) (of x itself if s = 0; infinities saturate, NaN is 0x7F);
+ *   where s grew, old codes = e4m3_satfinite(e4m3(code) * (s_old / s)) (fp32; a shift of the
+ *   exponent between powers of two, exact but for values that become subnormal).
+ *   K means over the block's rows up to seq_len: S_d = sum of e4m3(code) (exact; 0 for a
+ *   dimension with a NaN), ms = max_d |S_d| * fp32(1/127), k_mean = rint(S_d / ms) (0 if ms = 0),
+ *   k_mean_scale = ms * s / rows (fp32, each operation rounded to nearest).
+ *   k, v   (device) bf16 [B, T, nkv, hd], after RoPE; consecutive tokens kv_stride elements
+ *          apart (>= nkv * hd: slices of a fused projection), sequences T * kv_stride apart
+ * Rows behind seq_len in the last block are left as they were. Blocks that get rows must
+ * belong to one sequence alone (two writers of one block leave either's bytes). T >= 1. */
+mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, const uint16_t* v,
+                            int64_t kv_stride, int32_t B, int64_t T, const int32_t* seq_lens,
+                            const int32_t* q_lens, const int32_t* block_table, int64_t n_table,
+                            int32_t* dev_err, void* stream);
+
+/* mtp_block_attn -- attention of each sequence's tokens over its cached positions.
+ *   query head i of token t, kv head g = i / (nq / nkv), p < lim(b, t):
+ *   s_p = scale * sum_d q[b, t, i, d] k_scale e4m3(K[p, g, d]);  w = softmax(s)
+ *   out[b, t, i] = bf16(sum_p w_p v_scale e4m3(V[p, g]));  out_lse = log sum_p exp(s_p)
+ *   out_mass[b, j] = (mass ? mass[b, j] : 0) + sum over the tokens, heads and the positions of
+ *   logical block j of w_p, for every j < n_table
+ * fp32 sums and softmax statistics; the tensor cores take q as f16 scaled per head by a power
+ * of two (exact for elements above 2^-31 of the head's largest) and the weights
+ * exp(s_p - max) in (0, 1] rounded to f16, the same rounded weights in the denominator; lse
+ * and mass come from the unrounded ones. A token that sees no readable position gets zeros, lse -inf and no
+ * mass. What lies in masked rows (NaN included) changes nothing.
+ *   q        (device) bf16 [B, T, nq, hd], consecutive tokens q_stride elements apart
+ *            (>= nq * hd), sequences T * q_stride apart
+ *   out      (device) bf16 [B, T, nq, hd] contiguous; out_lse f32 [B, T, nq] or NULL
+ *   mass     (device) f32 [B, n_table] or NULL; out_mass the same or NULL (both may be one
+ *            buffer; mass without out_mass is MTP_ERR_INVALID_ARG)
+ *   ws       (device) >= mtp_block_attn_ws_bytes(cache, B, T, nq, n_table, with_mass) bytes,
+ *            16-byte aligned, no initial contents; with_mass = out_mass != NULL
+ * Requires nq % nkv == 0, nq / nkv <= 16, 1 <= T <= 64, scale >= 0. Results do not depend on
+ * the order in which blocks of the grid run: the same call gives the same bits. */
+size_t mtp_block_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T, int32_t nq,
+                               int64_t n_table, int32_t with_mass);
+mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,
+                          int32_t B, int32_t T, int32_t nq, const int32_t* seq_lens,
+                          const int32_t* q_lens, const int32_t* block_table, int64_t n_table,
+                          float scale, uint16_t* out, float* out_lse, const float* mass,
+                          float* out_mass, int32_t* dev_err, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* mtp_block_select -- the blocks each token attends to, by a cheap score of their mean keys.
+ * For token t of sequence b and kv head g, over its blocks j < ceil(lim(b, t) / block_size):
+ *   q8 = rint(q / sq), sq = max_d |q| * fp32(1/127) per query head (q8 = 0 if sq = 0);
+ *   score_j = max over the group's heads of float(q8 . k_mean_j) * (sq * k_mean_scale_j)
+ * (whole-number dot products; fp32, each operation rounded to nearest, so the choice is the
+ * same everywhere). The first n_first and the last n_last of those blocks are always taken, then
+ * the largest scores (of equal ones the lowest j) until n_sel are. A NaN score counts as the
+ * lowest, a head with an infinity or NaN in q does not count, a missing block scores lowest.
+ *   sel      (device) i32 [B, T, nkv, n_sel]: the chosen logical blocks ascending, then -1
+ *   ws       (device) >= mtp_block_select_ws_bytes(cache, B, T, n_table) bytes, 16-byte aligned
+ * The cache's k and v are not read and may be NULL here; its means are required. n_first >= 0,
+ * n_last >= 1, n_first + n_last <= n_sel (MTP_ERR_INVALID_ARG); q, nq and T as mtp_block_attn. */
+size_t mtp_block_select_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
+                                 int64_t n_table);
+mtp_status mtp_block_select(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,
+                            int32_t B, int32_t T, int32_t nq, const int32_t* seq_lens,
+                            const int32_t* q_lens, const int32_t* block_table, int64_t n_table,
+                            int32_t n_sel, int32_t n_first, int32_t n_last, int32_t* sel,
+                            int32_t* dev_err, void* ws, size_t ws_bytes, void* stream);
+
+/* mtp_block_sparse_attn -- mtp_block_attn over listed blocks only: token t and kv head g read
+ * the positions p < lim(b, t) of the logical blocks sel[b, t, g, :] (i32 [B, T, nkv, n_sel], as
+ * mtp_block_select writes it; negative entries are skipped, order does not matter, a block
+ * listed twice counts twice). No mass. ws >= mtp_block_sparse_attn_ws_bytes(...) bytes;
+ * n_sel * block_size <= 2^30; every other argument and rule is mtp_block_attn's. */
+size_t mtp_block_sparse_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
+                                      int32_t nq, int32_t n_sel);
+mtp_status mtp_block_sparse_attn(const mtp_block_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, int32_t B, int32_t T, int32_t nq,
+                                 const int32_t* seq_lens, const int32_t* q_lens,
+                                 const int32_t* block_table, int64_t n_table,
+                                 const int32_t* sel, int32_t n_sel, float scale, uint16_t* out,
+                                 float* out_lse, int32_t* dev_err, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* mtp_block_evict -- bounds each sequence to `keep` blocks by accumulated attention weight.
+ * A sequence with nb = ceil(seq_len / block_size) > keep blocks (at most n_table count) loses
+ * the nb - keep blocks of the smallest mass (of equal ones the lowest index; NaN counts as
+ * the smallest) among those that are neither its first n_first nor its last n_last. The others move up in
+ * order: out_table and out_mass hold the remaining blocks' entries, then -1 and 0;
+ * out_lens = seq_len - block_size * evicted; freed lists the physical blocks that left in
+ * order, then -1; n_freed their number. Cached rows do not move. A sequence within its bound
+ * is copied. mass as mtp_block_attn accumulates it.
+ *   block_table, out_table, freed (device) i32 [B, n_table]; seq_lens, out_lens, n_freed
+ *   (device) i32 [B]; mass, out_mass (device) f32 [B, n_table]. An output may be its own
+ *   input (in place); otherwise they must not overlap.
+ * Requires block_size >= 1, n_first >= 0, n_last >= 1, n_first + n_last <= keep
+ * (MTP_ERR_INVALID_ARG otherwise). */
+mtp_status mtp_block_evict(int32_t B, const int32_t* block_table, int64_t n_table,
+                           const int32_t* seq_lens, const float* mass, int32_t block_size,
+                           int32_t keep, int32_t n_first, int32_t n_last, int32_t* out_table,
+                           int32_t* out_lens, float* out_mass, int32_t* freed, int32_t* n_freed,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------------
  * Stage checks of the prefill, each through the code the prefill itself runs:
  * mtp_debug_gemm_bf16: C = bf16(A . B^T), A bf16 [M, K], B bf16 [N, K], C bf16 [M, N]
  *   (the tcgen05 GEMM); requires N % 256 == 0, K % 64 == 0, 16-byte aligned pointers.

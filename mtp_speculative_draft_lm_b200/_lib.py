@@ -45,6 +45,9 @@ EXPORTS = (
     "mtp_paged_decode_attn",
     "mtp_noalloc_scratch_bytes", "mtp_lm_head_argmax_noalloc",
     "mtp_prefill_ws_bytes", "mtp_prefill_kv", "mtp_debug_gemm_bf16", "mtp_debug_kv_write",
+    "mtp_block_append", "mtp_block_attn_ws_bytes", "mtp_block_attn", "mtp_block_select_ws_bytes",
+    "mtp_block_select", "mtp_block_sparse_attn_ws_bytes", "mtp_block_sparse_attn",
+    "mtp_block_evict",
 )
 
 
@@ -60,11 +63,20 @@ class mtp_weight(C.Structure):
                 ("block_scale", C.c_void_p), ("global_scale", C.c_void_p)]
 
 
+class mtp_block_cache(C.Structure):
+    _fields_ = [("nkv", C.c_int32), ("hd", C.c_int32), ("block_size", C.c_int32),
+                ("reserved", C.c_int32), ("num_blocks", C.c_int64), ("block_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("row_stride", C.c_int64), ("k", C.c_void_p),
+                ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("k_mean", C.c_void_p), ("k_mean_scale", C.c_void_p)]
+
+
 _P = C.c_void_p
 _I32 = C.c_int32
 _I64 = C.c_int64
 _SZ = C.c_size_t
 _W = C.POINTER(mtp_weight)
+_BC = C.POINTER(mtp_block_cache)
 
 _SIGS = {
     "mtp_abi_version": (_I32, []),
@@ -104,6 +116,18 @@ _SIGS = {
                                         _P]),
     "mtp_draft_step": (C.c_int, [_P, _I64, _P, _P, _I32, _I32, _P, _P, C.c_float, _I32, _P, _P,
                                  _I64, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+    "mtp_block_append": (C.c_int, [_BC, _P, _P, _I64, _I32, _I64, _P, _P, _P, _I64, _P, _P]),
+    "mtp_block_attn_ws_bytes": (_SZ, [_BC, _I32, _I32, _I32, _I64, _I32]),
+    "mtp_block_attn": (C.c_int, [_BC, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, C.c_float, _P,
+                                 _P, _P, _P, _P, _P, _SZ, _P]),
+    "mtp_block_select_ws_bytes": (_SZ, [_BC, _I32, _I32, _I64]),
+    "mtp_block_select": (C.c_int, [_BC, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _I32, _I32,
+                                   _I32, _P, _P, _P, _SZ, _P]),
+    "mtp_block_sparse_attn_ws_bytes": (_SZ, [_BC, _I32, _I32, _I32, _I32]),
+    "mtp_block_sparse_attn": (C.c_int, [_BC, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _I64, _P,
+                                        _I32, C.c_float, _P, _P, _P, _P, _SZ, _P]),
+    "mtp_block_evict": (C.c_int, [_I32, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                                  _P, _P]),
     "mtp_debug_encode_e4m3": (C.c_int, [_P, _I64, _P, _P]),
     "mtp_debug_encode_e2m1": (C.c_int, [_P, _I64, _P, _P]),
 }
@@ -318,6 +342,62 @@ def mtp_paged_decode_attn(q, nq, nkv, hd, k_cache, v_cache, block_table, n_table
                                         seq_len, float(k_scale), float(v_scale), float(scale),
                                         _ptr(out), _ptr(dev_err), _ptr(ws), ws_bytes,
                                         _stream(stream)), "mtp_paged_decode_attn")
+
+
+def _cache(c):
+    return C.byref(c) if c is not None else None
+
+
+def mtp_block_append(cache, k, v, kv_stride, B, T, seq_lens, q_lens, block_table, n_table,
+                     dev_err=None, stream=None):
+    _check(load().mtp_block_append(_cache(cache), _ptr(k), _ptr(v), kv_stride, B, T, _ptr(seq_lens),
+                                   _ptr(q_lens), _ptr(block_table), n_table, _ptr(dev_err),
+                                   _stream(stream)), "mtp_block_append")
+
+
+def mtp_block_attn_ws_bytes(cache, B, T, nq, n_table, with_mass) -> int:
+    return load().mtp_block_attn_ws_bytes(_cache(cache), B, T, nq, n_table, int(with_mass))
+
+
+def mtp_block_attn(cache, q, q_stride, B, T, nq, seq_lens, q_lens, block_table, n_table, scale,
+                   out, out_lse, mass, out_mass, dev_err, ws, ws_bytes, stream=None):
+    _check(load().mtp_block_attn(_cache(cache), _ptr(q), q_stride, B, T, nq, _ptr(seq_lens),
+                                 _ptr(q_lens), _ptr(block_table), n_table, float(scale), _ptr(out),
+                                 _ptr(out_lse), _ptr(mass), _ptr(out_mass), _ptr(dev_err), _ptr(ws),
+                                 ws_bytes, _stream(stream)), "mtp_block_attn")
+
+
+def mtp_block_select_ws_bytes(cache, B, T, n_table) -> int:
+    return load().mtp_block_select_ws_bytes(_cache(cache), B, T, n_table)
+
+
+def mtp_block_select(cache, q, q_stride, B, T, nq, seq_lens, q_lens, block_table, n_table, n_sel,
+                     n_first, n_last, sel, dev_err, ws, ws_bytes, stream=None):
+    _check(load().mtp_block_select(_cache(cache), _ptr(q), q_stride, B, T, nq, _ptr(seq_lens),
+                                   _ptr(q_lens), _ptr(block_table), n_table, n_sel, n_first, n_last,
+                                   _ptr(sel), _ptr(dev_err), _ptr(ws), ws_bytes, _stream(stream)),
+           "mtp_block_select")
+
+
+def mtp_block_sparse_attn_ws_bytes(cache, B, T, nq, n_sel) -> int:
+    return load().mtp_block_sparse_attn_ws_bytes(_cache(cache), B, T, nq, n_sel)
+
+
+def mtp_block_sparse_attn(cache, q, q_stride, B, T, nq, seq_lens, q_lens, block_table, n_table,
+                          sel, n_sel, scale, out, out_lse, dev_err, ws, ws_bytes, stream=None):
+    _check(load().mtp_block_sparse_attn(_cache(cache), _ptr(q), q_stride, B, T, nq, _ptr(seq_lens),
+                                        _ptr(q_lens), _ptr(block_table), n_table, _ptr(sel), n_sel,
+                                        float(scale), _ptr(out), _ptr(out_lse), _ptr(dev_err),
+                                        _ptr(ws), ws_bytes, _stream(stream)),
+           "mtp_block_sparse_attn")
+
+
+def mtp_block_evict(B, block_table, n_table, seq_lens, mass, block_size, keep, n_first, n_last,
+                    out_table, out_lens, out_mass, freed, n_freed, stream=None):
+    _check(load().mtp_block_evict(B, _ptr(block_table), n_table, _ptr(seq_lens), _ptr(mass),
+                                  block_size, keep, n_first, n_last, _ptr(out_table),
+                                  _ptr(out_lens), _ptr(out_mass), _ptr(freed), _ptr(n_freed),
+                                  _stream(stream)), "mtp_block_evict")
 
 
 def mtp_debug_wait_timeout(which, limit_cycles, counter, dev_err, stream=None):

@@ -254,6 +254,140 @@ def paged_decode_attn(q, nkv, k_cache, v_cache, block_table, seq_len, k_scale=1.
     return out, ws
 
 
+@dataclass
+class BlockCache:
+    """A block-scaled paged cache: E4M3 codes k, v with logical shape [num_blocks, nkv,
+    block_size, hd] (uint8, any strides with hd contiguous), fp32 scales [num_blocks, nkv] and,
+    for block selection, 8-bit mean keys [num_blocks, nkv, hd] with their scales."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    k_mean: torch.Tensor | None = None
+    k_mean_scale: torch.Tensor | None = None
+    desc: L.mtp_block_cache = field(init=False)
+
+    def __post_init__(self):
+        nb, nkv, bs, hd = self.k.shape
+        assert self.k.dtype == self.v.dtype == torch.uint8 and self.v.shape == self.k.shape
+        assert self.k.stride() == self.v.stride() and self.k.stride(3) == 1
+        for t in (self.k_scale, self.v_scale, self.k_mean_scale):
+            assert t is None or (t.shape == (nb, nkv) and t.dtype == torch.float32 and t.is_contiguous())
+        m = self.k_mean
+        assert m is None or (m.shape == (nb, nkv, hd) and m.dtype == torch.int8 and m.is_contiguous())
+        self.desc = L.mtp_block_cache(nkv, hd, bs, 0, nb, self.k.stride(0), self.k.stride(1),
+                                      self.k.stride(2), *(L._ptr(t) for t in (
+                                          self.k, self.v, self.k_scale, self.v_scale, self.k_mean,
+                                          self.k_mean_scale)))
+
+    @classmethod
+    def empty(cls, num_blocks: int, nkv: int, hd: int, block_size: int = 16, device="cuda"):
+        """A cache with its codes, scales and means zero, one block's rows of a head contiguous."""
+        z = lambda shape, t: torch.zeros(shape, dtype=t, device=device)  # noqa: E731
+        n = (num_blocks, nkv)
+        return cls(z(n + (block_size, hd), torch.uint8), z(n + (block_size, hd), torch.uint8),
+                   z(n, torch.float32), z(n, torch.float32), z(n + (hd,), torch.int8),
+                   z(n, torch.float32))
+
+    @classmethod
+    def of(cls, k, v, k_scale, v_scale, k_mean=None, k_mean_scale=None):
+        """Over tensors the caller has."""
+        return cls(k, v, k_scale, v_scale, k_mean, k_mean_scale)
+
+    @classmethod
+    def of_prefill(cls, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float = 1.0,
+                   v_scale: float = 1.0):
+        """Over the [num_blocks, block_size, nkv, hd] cache that prefill_kv writes, every block
+        and head at the call's one scale. It has no means (block_select needs them)."""
+        nb, _, nkv, _ = k_cache.shape
+        ks = torch.full((nb, nkv), float(k_scale), dtype=torch.float32, device=k_cache.device)
+        return cls(k_cache.transpose(1, 2), v_cache.transpose(1, 2), ks,
+                   torch.full_like(ks, float(v_scale)))
+
+
+def _token_stride(x: torch.Tensor) -> int:
+    """Elements between the tokens of x [B, T, heads, hd], whose heads are packed."""
+    B, T, _, hd = x.shape
+    st = x.stride()
+    if x.dtype != torch.bfloat16 or st[3] != 1 or (x.shape[2] > 1 and st[2] != hd):
+        raise ValueError("expected bf16 [B, T, heads, hd] with packed heads")
+    step = st[1] if T > 1 else st[0] if B > 1 else x.shape[2] * hd
+    if B > 1 and st[0] != T * step:
+        raise ValueError("sequences must be T token strides apart")
+    return step
+
+
+def _block_ws(ws, nbytes: int, device):
+    return torch.empty((nbytes,), dtype=torch.uint8, device=device) if ws is None or ws.numel() < nbytes else ws
+
+
+def block_append(cache: BlockCache, k, v, block_table, seq_lens, q_lens=None, dev_err=None,
+                 stream=None):
+    """Writes the new rows k, v [B, T, nkv, hd] (bf16, slices of a projection allowed) at the end
+    of each sequence (seq_lens counts them already) and updates scales and means."""
+    B, T = k.shape[:2]
+    step = _token_stride(k)
+    if k.shape != v.shape or _token_stride(v) != step or k.shape[2] != cache.desc.nkv or k.shape[3] != cache.desc.hd:
+        raise ValueError("k and v must be the cache's heads with one stride")
+    L.mtp_block_append(cache.desc, k, v, step, B, T, seq_lens, q_lens, block_table,
+                       block_table.shape[1], dev_err, stream)
+
+
+def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=None, out=None,
+               out_lse=None, mass=None, out_mass=None, ws=None, dev_err=None, stream=None):
+    """Attention of q [B, T, nq, hd] over each sequence's cached positions (causal among the T
+    tokens); out_mass accumulates each block's softmax weight. Returns (out, ws)."""
+    B, T, nq, hd = q.shape
+    out = torch.empty((B, T, nq, hd), dtype=torch.bfloat16, device=q.device) if out is None else out
+    n_table = block_table.shape[1]
+    ws = _block_ws(ws, L.mtp_block_attn_ws_bytes(cache.desc, B, T, nq, n_table, out_mass is not None), q.device)
+    L.mtp_block_attn(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table, n_table,
+                     1.0 / float(hd) ** 0.5 if scale is None else scale, out, out_lse, mass, out_mass,
+                     dev_err, ws, ws.numel(), stream)
+    return out, ws
+
+
+def block_select(cache: BlockCache, q, block_table, seq_lens, n_sel, n_first=1, n_last=1,
+                 q_lens=None, out=None, ws=None, dev_err=None, stream=None):
+    """The n_sel blocks that each token and kv head attends to, by the 8-bit product of its
+    query heads with the blocks' mean keys: (sel [B, T, nkv, n_sel] i32, ws)."""
+    B, T, nq, _ = q.shape
+    n_table = block_table.shape[1]
+    out = torch.empty((B, T, cache.desc.nkv, n_sel), dtype=torch.int32, device=q.device) if out is None else out
+    ws = _block_ws(ws, L.mtp_block_select_ws_bytes(cache.desc, B, T, n_table), q.device)
+    L.mtp_block_select(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table, n_table,
+                       n_sel, n_first, n_last, out, dev_err, ws, ws.numel(), stream)
+    return out, ws
+
+
+def block_sparse_attn(cache: BlockCache, q, block_table, seq_lens, sel, q_lens=None, scale=None,
+                      out=None, out_lse=None, ws=None, dev_err=None, stream=None):
+    """block_attn over the blocks that sel [B, T, nkv, n_sel] lists. Returns (out, ws)."""
+    B, T, nq, hd = q.shape
+    out = torch.empty((B, T, nq, hd), dtype=torch.bfloat16, device=q.device) if out is None else out
+    n_sel = sel.shape[3]
+    ws = _block_ws(ws, L.mtp_block_sparse_attn_ws_bytes(cache.desc, B, T, nq, n_sel), q.device)
+    L.mtp_block_sparse_attn(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table,
+                            block_table.shape[1], sel, n_sel,
+                            1.0 / float(hd) ** 0.5 if scale is None else scale, out, out_lse, dev_err,
+                            ws, ws.numel(), stream)
+    return out, ws
+
+
+def block_evict(block_table, seq_lens, mass, block_size, keep, n_first=1, n_last=1, out_table=None,
+                out_lens=None, out_mass=None, freed=None, n_freed=None, stream=None):
+    """Bounds each sequence to `keep` blocks by accumulated weight: (out_table, out_lens,
+    out_mass, freed, n_freed). Outputs may be the inputs (in place)."""
+    B, n_table = block_table.shape
+    new = lambda t, like: torch.empty_like(like) if t is None else t  # noqa: E731
+    out_table, freed = new(out_table, block_table), new(freed, block_table)
+    out_lens, n_freed = new(out_lens, seq_lens), new(n_freed, seq_lens)
+    out_mass = new(out_mass, mass)
+    L.mtp_block_evict(B, block_table, n_table, seq_lens, mass, block_size, keep, n_first, n_last,
+                      out_table, out_lens, out_mass, freed, n_freed, stream)
+    return out_table, out_lens, out_mass, freed, n_freed
+
+
 def aligned_empty(nbytes: int, align: int, device) -> torch.Tensor:
     """A uint8 device buffer of nbytes whose address is a multiple of align (torch only
     promises 512 bytes)."""

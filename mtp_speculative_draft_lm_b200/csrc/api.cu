@@ -373,6 +373,182 @@ mtp_status mtp_paged_decode_attn(const uint16_t* q, int32_t nq, int32_t nkv, int
                                       out, dev_err, ws, as_stream(stream)));
 }
 
+namespace {
+
+// Checks a block cache's descriptor. with_codes: the call reads or writes k, v and their
+// scales; with_means: it needs the means.
+mtp_status check_block_cache(const mtp_block_cache* c, bool with_codes, bool with_means) {
+    if (!c || c->reserved != 0 || c->nkv < 1 || c->hd < 1 || c->block_size < 1 || c->num_blocks < 1)
+        return MTP_ERR_INVALID_ARG;
+    if ((c->k_mean == nullptr) != (c->k_mean_scale == nullptr)) return MTP_ERR_INVALID_ARG;
+    if (!aligned(c->k_mean, 16) || !aligned(c->k_mean_scale, 4)) return MTP_ERR_INVALID_ARG;
+    if (with_means && !c->k_mean) return MTP_ERR_INVALID_ARG;
+    if (with_codes) {
+        if (!c->k || !c->v || !c->k_scale || !c->v_scale) return MTP_ERR_INVALID_ARG;
+        if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+            return MTP_ERR_INVALID_ARG;
+        if (c->block_stride < 1 || c->head_stride < 1 || c->row_stride < c->hd || c->block_stride % 16 ||
+            c->head_stride % 16 || c->row_stride % 16)
+            return MTP_ERR_INVALID_ARG;
+    }
+    if ((c->hd != 64 && c->hd != 128 && c->hd != 256) ||
+        (c->block_size != 16 && c->block_size != 32 && c->block_size != 64) || c->nkv > 4096 ||
+        c->num_blocks > (int64_t)INT32_MAX)
+        return MTP_ERR_UNSUPPORTED;
+    // strides that a tensor copy's 40-bit fields hold, with room for 64-bit byte offsets
+    if (with_codes && (c->block_stride >= (int64_t)1 << 39 || c->head_stride >= (int64_t)1 << 39 ||
+                       c->row_stride >= (int64_t)1 << 39 || c->num_blocks * (c->block_stride >> 4) >= (int64_t)1 << 56))
+        return MTP_ERR_UNSUPPORTED;
+    return MTP_OK;
+}
+
+mtp_status check_block_batch(const mtp_block_cache* c, int32_t B, int64_t T, const int32_t* seq_lens,
+                             const int32_t* q_lens, const int32_t* table, int64_t n_table,
+                             const int32_t* dev_err) {
+    if (B < 1 || T < 1 || !seq_lens || !table || n_table < 1) return MTP_ERR_INVALID_ARG;
+    if (!aligned(seq_lens, 4) || !aligned(q_lens, 4) || !aligned(table, 4) || !aligned(dev_err, 4))
+        return MTP_ERR_INVALID_ARG;
+    if (B > 65535 || n_table > ((int64_t)1 << 30) / c->block_size) return MTP_ERR_UNSUPPORTED;
+    return MTP_OK;
+}
+
+// The query side of attention and selection.
+mtp_status check_block_query(const mtp_block_cache* c, const uint16_t* q, int64_t q_stride, int64_t T,
+                             int32_t nq) {
+    if (!q || nq < 1 || nq % c->nkv || q_stride < (int64_t)nq * c->hd || q_stride % 8 || !aligned(q, 16))
+        return MTP_ERR_INVALID_ARG;
+    if (nq / c->nkv > mtp::block_attn_max_group() || T > mtp::block_attn_max_t() ||
+        q_stride > (int64_t)1 << 40)
+        return MTP_ERR_UNSUPPORTED;
+    return MTP_OK;
+}
+
+mtp::BlockCache to_cache(const mtp_block_cache* c) {
+    return {c->nkv, c->hd, c->block_size, c->num_blocks, c->block_stride, c->head_stride, c->row_stride,
+            c->k, c->v, c->k_scale, c->v_scale, c->k_mean, c->k_mean_scale};
+}
+
+mtp_status block_attn_impl(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride, int32_t B,
+                           int32_t T, int32_t nq, const int32_t* seq_lens, const int32_t* q_lens,
+                           const int32_t* table, int64_t n_table, const int32_t* sel, int32_t n_sel,
+                           bool sparse, float scale, uint16_t* out, float* out_lse, const float* mass,
+                           float* out_mass, int32_t* dev_err, void* ws, size_t ws_bytes, void* stream) {
+    mtp_status st = check_block_cache(cache, true, false);
+    if (st != MTP_OK) return st;
+    if ((st = check_block_batch(cache, B, T, seq_lens, q_lens, table, n_table, dev_err)) != MTP_OK) return st;
+    if ((st = check_block_query(cache, q, q_stride, T, nq)) != MTP_OK) return st;
+    if (!out || !aligned(out, 16) || !aligned(out_lse, 4) || !aligned(mass, 4) || !aligned(out_mass, 4) ||
+        (mass && !out_mass) || !(scale >= 0.f) || !(scale < 3.0e38f))
+        return MTP_ERR_INVALID_ARG;
+    if (sparse) {
+        if (!sel || n_sel < 1 || !aligned(sel, 4)) return MTP_ERR_INVALID_ARG;
+        if ((int64_t)n_sel * cache->block_size > (int64_t)1 << 30) return MTP_ERR_UNSUPPORTED;
+    }
+    const mtp::BlockCache c = to_cache(cache);
+    if (!ws || !aligned(ws, 16) ||
+        ws_bytes < mtp::block_attn_ws_bytes(c, B, T, nq, n_table, n_sel, sparse, out_mass != nullptr))
+        return MTP_ERR_WORKSPACE;
+    const mtp::BlockBatch t{B, T, seq_lens, q_lens, table, n_table, dev_err};
+    const mtp::BlockAttnArgs a{q, q_stride, nq, scale, sparse ? sel : nullptr, n_sel, out, out_lse, mass,
+                               out_mass, ws};
+    return from_cuda(mtp::block_attn_launch(c, t, a, as_stream(stream)));
+}
+
+}  // namespace
+
+mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, const uint16_t* v,
+                            int64_t kv_stride, int32_t B, int64_t T, const int32_t* seq_lens,
+                            const int32_t* q_lens, const int32_t* block_table, int64_t n_table,
+                            int32_t* dev_err, void* stream) {
+    mtp_status st = check_block_cache(cache, true, false);
+    if (st != MTP_OK) return st;
+    if ((st = check_block_batch(cache, B, T, seq_lens, q_lens, block_table, n_table, dev_err)) != MTP_OK)
+        return st;
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || kv_stride % 8 ||
+        kv_stride < (int64_t)cache->nkv * cache->hd)
+        return MTP_ERR_INVALID_ARG;
+    if (T > (int64_t)1 << 30 || kv_stride > (int64_t)1 << 40) return MTP_ERR_UNSUPPORTED;
+    const mtp::BlockBatch t{B, T, seq_lens, q_lens, block_table, n_table, dev_err};
+    return from_cuda(mtp::block_append_launch(to_cache(cache), t, k, v, kv_stride, as_stream(stream)));
+}
+
+size_t mtp_block_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T, int32_t nq,
+                               int64_t n_table, int32_t with_mass) {
+    if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || nq < 1 || n_table < 1) return 0;
+    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, n_table, 0, false, with_mass != 0);
+}
+
+mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,
+                          int32_t B, int32_t T, int32_t nq, const int32_t* seq_lens,
+                          const int32_t* q_lens, const int32_t* block_table, int64_t n_table,
+                          float scale, uint16_t* out, float* out_lse, const float* mass,
+                          float* out_mass, int32_t* dev_err, void* ws, size_t ws_bytes,
+                          void* stream) {
+    return block_attn_impl(cache, q, q_stride, B, T, nq, seq_lens, q_lens, block_table, n_table, nullptr, 0,
+                           false, scale, out, out_lse, mass, out_mass, dev_err, ws, ws_bytes, stream);
+}
+
+size_t mtp_block_sparse_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
+                                      int32_t nq, int32_t n_sel) {
+    if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || nq < 1 || n_sel < 1) return 0;
+    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, 1, n_sel, true, false);
+}
+
+mtp_status mtp_block_sparse_attn(const mtp_block_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, int32_t B, int32_t T, int32_t nq,
+                                 const int32_t* seq_lens, const int32_t* q_lens,
+                                 const int32_t* block_table, int64_t n_table,
+                                 const int32_t* sel, int32_t n_sel, float scale, uint16_t* out,
+                                 float* out_lse, int32_t* dev_err, void* ws, size_t ws_bytes,
+                                 void* stream) {
+    return block_attn_impl(cache, q, q_stride, B, T, nq, seq_lens, q_lens, block_table, n_table, sel, n_sel,
+                           true, scale, out, out_lse, nullptr, nullptr, dev_err, ws, ws_bytes, stream);
+}
+
+size_t mtp_block_select_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
+                                 int64_t n_table) {
+    if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || n_table < 1) return 0;
+    return mtp::block_select_ws_bytes(to_cache(cache), B, T, n_table);
+}
+
+mtp_status mtp_block_select(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,
+                            int32_t B, int32_t T, int32_t nq, const int32_t* seq_lens,
+                            const int32_t* q_lens, const int32_t* block_table, int64_t n_table,
+                            int32_t n_sel, int32_t n_first, int32_t n_last, int32_t* sel,
+                            int32_t* dev_err, void* ws, size_t ws_bytes, void* stream) {
+    mtp_status st = check_block_cache(cache, false, true);
+    if (st != MTP_OK) return st;
+    if ((st = check_block_batch(cache, B, T, seq_lens, q_lens, block_table, n_table, dev_err)) != MTP_OK)
+        return st;
+    if ((st = check_block_query(cache, q, q_stride, T, nq)) != MTP_OK) return st;
+    if (!sel || !aligned(sel, 4) || n_first < 0 || n_last < 1 || (int64_t)n_first + n_last > n_sel)
+        return MTP_ERR_INVALID_ARG;
+    const mtp::BlockCache c = to_cache(cache);
+    if (!ws || !aligned(ws, 16) || ws_bytes < mtp::block_select_ws_bytes(c, B, T, n_table))
+        return MTP_ERR_WORKSPACE;
+    const mtp::BlockBatch t{B, T, seq_lens, q_lens, block_table, n_table, dev_err};
+    return from_cuda(mtp::block_select_launch(c, t, q, q_stride, nq, n_sel, n_first, n_last, sel, ws,
+                                              as_stream(stream)));
+}
+
+mtp_status mtp_block_evict(int32_t B, const int32_t* block_table, int64_t n_table,
+                           const int32_t* seq_lens, const float* mass, int32_t block_size,
+                           int32_t keep, int32_t n_first, int32_t n_last, int32_t* out_table,
+                           int32_t* out_lens, float* out_mass, int32_t* freed, int32_t* n_freed,
+                           void* stream) {
+    if (!block_table || !seq_lens || !mass || !out_table || !out_lens || !out_mass || !freed || !n_freed)
+        return MTP_ERR_INVALID_ARG;
+    if (B < 1 || n_table < 1 || block_size < 1 || n_first < 0 || n_last < 1 || (int64_t)n_first + n_last > keep)
+        return MTP_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(mass, 4) || !aligned(out_table, 4) ||
+        !aligned(out_lens, 4) || !aligned(out_mass, 4) || !aligned(freed, 4) || !aligned(n_freed, 4))
+        return MTP_ERR_INVALID_ARG;
+    if (B > 65535 || n_table > ((int64_t)1 << 30) / block_size) return MTP_ERR_UNSUPPORTED;
+    return from_cuda(mtp::block_evict_launch(B, block_table, n_table, seq_lens, mass, block_size, keep, n_first,
+                                             n_last, out_table, out_lens, out_mass, freed, n_freed,
+                                             as_stream(stream)));
+}
+
 size_t mtp_prefill_ws_bytes(int64_t chunk_rows, int32_t h, int32_t nkv, int32_t hd) {
     if (chunk_rows < 1 || h < 1 || nkv < 1 || hd < 2) return 0;
     return mtp::prefill_ws_bytes(chunk_rows, h, nkv, hd);

@@ -163,6 +163,58 @@ cudaError_t attn_launch(const uint16_t* q, int nq, int nkv, int hd, const uint8_
                         float v_scale, float scale, uint16_t* out, int32_t* dev_err, void* ws,
                         cudaStream_t s);
 
+// The block-scaled paged cache (block_*.cu): its layout, and a batch's tokens over it.
+struct BlockCache {
+    int nkv, hd, bs;
+    int64_t num_blocks;
+    int64_t block_stride, head_stride, row_stride;  // bytes
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;  // [num_blocks, nkv]
+    float* v_scale;
+    int8_t* k_mean;  // [num_blocks, nkv, hd] or null
+    float* k_mean_scale;
+};
+struct BlockBatch {
+    int B;
+    int64_t T;                // token slots per sequence
+    const int32_t* seq_lens;  // [B]
+    const int32_t* q_lens;    // [B] or null (= T)
+    const int32_t* table;     // [B, n_table]
+    int64_t n_table;
+    int32_t* dev_err;
+};
+cudaError_t block_append_launch(const BlockCache& c, const BlockBatch& t, const uint16_t* k,
+                                const uint16_t* v, int64_t kv_stride, cudaStream_t s);
+// q and the outputs of an attention call; sel null: every block, else [B, T, nkv, n_sel].
+struct BlockAttnArgs {
+    const uint16_t* q;
+    int64_t q_stride;
+    int nq;
+    float scale;
+    const int32_t* sel;
+    int n_sel;
+    uint16_t* out;
+    float* out_lse;
+    const float* mass;
+    float* out_mass;
+    void* ws;
+};
+int block_attn_max_group();
+int block_attn_max_t();
+size_t block_attn_ws_bytes(const BlockCache& c, int B, int T, int nq, int64_t n_table, int n_sel,
+                           bool sparse, bool mass);
+cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const BlockAttnArgs& a,
+                              cudaStream_t s);
+size_t block_select_ws_bytes(const BlockCache& c, int B, int T, int64_t n_table);
+cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const uint16_t* q,
+                                int64_t q_stride, int nq, int n_sel, int n_first, int n_last,
+                                int32_t* sel, void* ws, cudaStream_t s);
+cudaError_t block_evict_launch(int B, const int32_t* table, int64_t n_table,
+                               const int32_t* seq_lens, const float* mass, int bs, int keep,
+                               int n_first, int n_last, int32_t* out_table, int32_t* out_lens,
+                               float* out_mass, int32_t* freed, int32_t* n_freed, cudaStream_t s);
+
 // Self-check of the bounded waits (selfcheck.cu): which 0 waits on an mbarrier phase that
 // nothing completes, 1 on a global counter (device u32, kept at 0 by the caller) that
 // nothing increments; either gives up after limit_cycles and sets DEVFLAG_TIMEOUT.
