@@ -446,7 +446,7 @@ mtp_status block_attn_impl(const mtp_block_cache* cache, const uint16_t* q, int6
     }
     const mtp::BlockCache c = to_cache(cache);
     if (!ws || !aligned(ws, 16) ||
-        ws_bytes < mtp::block_attn_ws_bytes(c, B, T, nq, n_table, n_sel, sparse, out_mass != nullptr))
+        ws_bytes < mtp::block_attn_ws_bytes(c, B, T, nq, n_table, sparse, out_mass != nullptr))
         return MTP_ERR_WORKSPACE;
     const mtp::BlockBatch t{B, T, seq_lens, q_lens, table, n_table, dev_err};
     const mtp::BlockAttnArgs a{q, q_stride, nq, scale, sparse ? sel : nullptr, n_sel, out, out_lse, mass,
@@ -475,7 +475,7 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
 size_t mtp_block_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T, int32_t nq,
                                int64_t n_table, int32_t with_mass) {
     if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || nq < 1 || n_table < 1) return 0;
-    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, n_table, 0, false, with_mass != 0);
+    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, n_table, false, with_mass != 0);
 }
 
 mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,
@@ -491,7 +491,7 @@ mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64
 size_t mtp_block_sparse_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
                                       int32_t nq, int32_t n_sel) {
     if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || nq < 1 || n_sel < 1) return 0;
-    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, 1, n_sel, true, false);
+    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, 1, true, false);
 }
 
 mtp_status mtp_block_sparse_attn(const mtp_block_cache* cache, const uint16_t* q,

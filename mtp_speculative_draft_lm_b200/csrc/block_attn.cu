@@ -1,9 +1,32 @@
 // Attention over the block-scaled paged cache (mtp_block_attn, mtp_block_sparse_attn).
 //
-// One warp per query head of a token: an online softmax over the positions it sees, the head's
-// dimensions spread over the lanes.
+// Mathematics, per query row r (a token's query head) and kv head g, in base 2:
+//   s_p = (scale log2(e)) k_scale[block] sum_d q[r, d] e4m3(K[p, d]);  w_p = 2^(s_p - m)
+//   out = sum_p w_p v_scale[block] e4m3(V[p]) / sum_p w_p,  lse = (m + log2(sum_p w_p)) ln 2
+// with any reference m: a running one, raised only when a score exceeds it by more than 8
+// binades (weights stay below 2^8, inside f16), so that most tiles need no maximum, no shuffle
+// and no rescaling, just one vote. A block's v_scale is not folded into the weights (they would
+// lose f16 bits): the accumulators are held in units of the current block's v_scale and change
+// units when it changes, an exact shift for powers of two.
+//
+// Work: the cache is read in tiles of 16 positions, each inside one block. A unit is a kv head
+// of a sequence with up to 8 NT of its T (nq / nkv) query rows (for listed blocks: of a
+// token). All units' tiles form one line; each CTA takes an equal stretch of it, however
+// ragged the batch. A unit that lies in one CTA is finished there; the others' partial sums go
+// to the workspace and a second kernel joins them in order of the CTAs (fixed order: the same
+// bits every time).
+//
+// Bound by HBM: every code is read once per row tile. Each of a CTA's four warps owns a ring of
+// tile stages (K and V, 16 rows each): it takes every fourth tile of the stretch, looks up its
+// blocks ahead and issues their tensor copies into the stage it has just used, across units,
+// so the warps meet only at a unit's end. Both contractions run on mma.sync m16n8k16 in f16 with fp32 sums: a tile has at most 32
+// query rows, far from where tcgen05's 128-row tiles would pay, and E4M3 decodes to f16
+// exactly (q is scaled per row by a power of two).
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <mutex>
 
 #include "block_cache.cuh"
 #include "common.cuh"
@@ -16,72 +39,752 @@ constexpr int kMaxGroup = 16;
 constexpr int kMaxT = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxGrid = 640;                  // CTAs (workspace slots are sized for it)
+constexpr float kRaise = 8.f;                  // binades a score may exceed the reference by
 
 struct AttnParams {
     BlockCache c;
     BlockBatch t;
     BlockAttnArgs a;
     int group;
-    int tiles;        // 16-position tiles of n_table blocks
-    float* row_lse;   // [B, T, nq] base-2 log-sum-exp (with mass)
-    float* tile_lse;  // [B, T, nq, tiles] (with mass)
+    int row_tiles;       // dense: row tiles of 8 NT rows that T tokens have at most
+    int64_t tiles;       // 16-position tiles of n_table blocks (tile_lse's pitch)
+    int64_t* per;        // [1] tiles per CTA
+    int64_t* unit_base;  // [units] first tile of each unit on the line
+    float* parts;        // [2 kMaxGrid][8 NT (hd + 4)] partial sums of a CTA's first and last unit
+    float* row_lse;      // [B, T, nq] base-2 log-sum-exp (with mass)
+    float* tile_lse;     // [B, T, nq, tiles] (with mass)
 };
 
-template <int HD>
-__global__ void __launch_bounds__(128) block_attn_simple_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int VEC = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t bt = w / p.a.nq;
-    const int i = (int)(w % p.a.nq);
-    const int b = (int)(bt / p.t.T), tok = (int)(bt % p.t.T);
-    if (b >= p.t.B) return;
+// A sequence's units and the tiles each has.
+struct SeqWork {
+    int len, q, units, tiles;
+};
+template <int NT, bool SPARSE>
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
     const SeqStep s = seq_step(p.t, b);
-    if (tok >= s.q) return;
-    const int lim = s.len - s.q + tok + 1;
-    const int g = i / p.group, bs = p.c.bs;
-    float q[VEC], acc[VEC], m = -INFINITY, l = 0.f;
-    for (int d = 0; d < VEC; ++d) {
-        q[d] = bf16_to_f32(p.a.q[bt * p.a.q_stride + (int64_t)i * HD + lane * VEC + d]);
-        acc[d] = 0.f;
+    SeqWork w{s.len, s.q, 0, 0};
+    if (SPARSE) {
+        w.units = s.q * p.c.nkv;
+        w.tiles = s.len > 0 ? p.a.n_sel * (p.c.bs / 16) : 0;
+    } else {
+        w.units = p.c.nkv * ((s.q * p.group + 8 * NT - 1) / (8 * NT));
+        const int nb = blocks_of(s.len, p.c.bs, p.t.n_table);
+        w.tiles = min((s.len + 15) / 16, nb * (p.c.bs / 16));
     }
-    const int entries = p.a.sel ? p.a.n_sel : blocks_of(lim, bs, p.t.n_table);
-    if (!p.a.sel && lim > 0 && (lim - 1) / bs >= p.t.n_table) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
-    for (int e = 0; e < entries; ++e) {
-        const int lb = p.a.sel ? p.a.sel[(bt * p.c.nkv + g) * p.a.n_sel + e] : e;
-        if (lb < 0) continue;
-        const int64_t pos0 = (int64_t)lb * bs;
-        const int n = table_block(p.t, p.c.num_blocks, b, lb);
-        if (pos0 < lim && n < 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
-        const int rows = n < 0 ? 0 : (int)max((int64_t)0, min((int64_t)bs, lim - pos0));
-        for (int t0 = 0; t0 < bs; t0 += 16) {
-            float tm = -INFINITY, tl = 0.f;
-            for (int r = t0; r < min(rows, t0 + 16); ++r) {
-                const float ks = p.c.k_scale[(int64_t)n * p.c.nkv + g], vs = p.c.v_scale[(int64_t)n * p.c.nkv + g];
-                const int64_t at = (int64_t)n * p.c.block_stride + (int64_t)g * p.c.head_stride + (int64_t)r * p.c.row_stride + lane * VEC;
-                float d = 0.f;
-                for (int u = 0; u < VEC; ++u) d = fmaf(q[u], e4m3_to_f32(p.c.k[at + u]), d);
-                for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                const float sc = d * (p.a.scale * ks) * kLog2e;
-                const float mn = fmaxf(m, sc);
-                const float al = m == -INFINITY ? 0.f : exp2f(m - mn), wt = exp2f(sc - mn);
-                l = l * al + wt;
-                for (int u = 0; u < VEC; ++u) acc[u] = acc[u] * al + wt * vs * e4m3_to_f32(p.c.v[at + u]);
-                m = mn;
-                const float tn = fmaxf(tm, sc);
-                tl = (tm == -INFINITY ? 0.f : tl * exp2f(tm - tn)) + exp2f(sc - tn);
-                tm = tn;
+    return w;
+}
+
+// The unit's index in unit_base: unit u of sequence b.
+template <bool SPARSE>
+__device__ __forceinline__ int64_t unit_index(const AttnParams& p, int b, int g, int part) {
+    return SPARSE ? ((int64_t)b * p.t.T + part) * p.c.nkv + g : ((int64_t)b * p.c.nkv + g) * p.row_tiles + part;
+}
+
+template <int HD, int NT>
+struct Shape {
+    static constexpr int kTile = 16 * HD;                       // bytes of K (or V) in a stage
+    static constexpr int kPerSm = HD == 256 || NT >= 2 ? 2 : 3;  // CTAs per SM
+    static constexpr int kQPitch = HD + 8;                      // f16 elements
+    static constexpr int kRows = 8 * NT;
+    static constexpr size_t kFixed = (size_t)HD * NT * 64         // two warps' accumulators
+                                     + (size_t)kRows * kQPitch * 2  // q
+                                     + (size_t)kRows * 8            // score factors, limits
+                                     + (size_t)3 * kWarps * kRows * 4 + 16;
+    static constexpr size_t kStage = (size_t)kWarps * (2 * kTile + 16 + 8);  // tiles, info, barriers
+    // (1 KB of each CTA's share of the SM's 228 KB is the system's)
+    static constexpr int kStages = (int)(((size_t)(228 * 1024) / kPerSm - 1024 - kFixed) / kStage);
+    static constexpr size_t kSmem = kStages * kStage + kFixed;
+    static_assert(kStages >= 2, "two stages at least");
+};
+
+struct TileInfo {
+    int pos0;  // first position, or -1: nothing to read
+    float ks, vs;
+    int pad;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+// Transpose of an 8 x 8 matrix of 16-bit values in the mma fragment layout.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ void copy4_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Arrive on `bar` (one of its expected arrivals) when this thread's earlier cp.async are done.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, int x, int row, int head, int block,
+                                          uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(row), "r"(head), "r"(block), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r in a stage's K or V tile, as the swizzled tensor
+// copies leave it: rows of 128 bytes (64 for hd = 64; hd = 256: two halves of 128).
+template <int HD>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+    if (HD == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+template <int HD, int NT, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
+    block_attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+    using S = Shape<HD, NT>;
+    constexpr int ST = S::kStages, KC = HD / 16, DT = HD / 16, R = S::kRows, QP = S::kQPitch;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t* ring = raw;  // [warp][stage][K, V][16 rows]
+    float4* xacc = reinterpret_cast<float4*>(ring + (size_t)kWarps * ST * 2 * S::kTile);  // [2][DT NT][32]
+    TileInfo* info = reinterpret_cast<TileInfo*>(xacc + 2 * DT * NT * 32);               // [warp][stage]
+    uint64_t* full = reinterpret_cast<uint64_t*>(info + kWarps * ST);                    // [warp][stage]
+    uint16_t* qh = reinterpret_cast<uint16_t*>(full + kWarps * ST);                      // [R][QP] f16
+    float* hfac = reinterpret_cast<float*>(qh + R * QP);                                 // [R]
+    int* lims = reinterpret_cast<int*>(hfac + R);                                        // [R]
+    float* redm = reinterpret_cast<float*>(lims + R);                                    // [warp][R]
+    float* redl = redm + kWarps * R;
+    float* redt = redl + kWarps * R;
+    volatile int* abort = reinterpret_cast<volatile int*>(redt + kWarps * R);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_launch_dependents();
+    if (smem_u32(raw) & 1023u) {  // (the swizzled copies need it; dynamic shared memory starts there)
+        if (tid == 0) raise_flag(p.t.dev_err, DEVFLAG_TIMEOUT);
+        return;
+    }
+    if (tid < kWarps * ST) mbar_init(&full[tid], 2);  // lane 0's arrival and its scale copies'
+    if (tid == 0) *abort = 0;
+    mbar_fence_init();
+    __syncthreads();
+    pdl_wait();  // everything below reads or writes memory that earlier kernels may still use
+
+    // this CTA's stretch of the line: [beg, end), its first sequence, unit and tile (every warp
+    // for itself: two passes over the lengths, 32 sequences at a time)
+    const int B = p.t.B;
+    int64_t total = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        int64_t n = 0;
+        if (b0 + lane < B) {
+            const SeqWork w = seq_work<NT, SPARSE>(p, b0 + lane);
+            n = (int64_t)w.units * w.tiles;
+        }
+        total += n;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    per = (per + kWarps - 1) / kWarps * kWarps;
+    if (blockIdx.x == 0 && tid == 0) *p.per = per;
+    const int64_t beg = (int64_t)blockIdx.x * per;
+    const int64_t stretch = min(total, beg + per) - beg;
+    if (stretch <= 0) return;
+    int b = 0, u = 0, t0 = 0;
+    {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            int64_t n = 0;
+            SeqWork w{0, 0, 0, 0};
+            if (b0 + lane < B) {
+                w = seq_work<NT, SPARSE>(p, b0 + lane);
+                n = (int64_t)w.units * w.tiles;
             }
-            if (p.a.out_mass && lane == 0)
-                p.tile_lse[(bt * p.a.nq + i) * p.tiles + (pos0 + t0) / 16] = tl > 0.f ? tm + log2f(tl) : -INFINITY;
+            int64_t inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, before + inc > beg);
+            if (past) {
+                const int src = __ffs(past) - 1;
+                const int64_t off = beg - (before + __shfl_sync(0xffffffffu, inc - n, src));
+                const int tiles = __shfl_sync(0xffffffffu, w.tiles, src);
+                b = b0 + src;
+                u = (int)(off / tiles);
+                t0 = (int)(off - (int64_t)u * tiles);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
         }
     }
-    for (int u = 0; u < VEC; ++u)
-        p.a.out[(bt * p.a.nq + i) * HD + lane * VEC + u] = f32_to_bf16(l > 0.f || l != l ? acc[u] / l : 0.f);
+    // A place on the line: a unit (kv head g; row tile or token `part`) and the tiles [t0, t1) of
+    // it that belong to this CTA.
+    struct Place {
+        SeqWork sw;
+        int b, u, g, part, t0, t1;
+        int64_t left;  // tiles of the stretch from t0 on
+    };
+    auto settle = [&](Place& c) {
+        if (SPARSE) {
+            c.part = c.u / p.c.nkv;
+            c.g = c.u - c.part * p.c.nkv;
+        } else {  // a head's row tiles in turn: the later ones find its tiles in L2
+            const int rt = c.sw.units / p.c.nkv;
+            c.g = c.u / rt;
+            c.part = c.u - c.g * rt;
+        }
+        c.t1 = (int)min((int64_t)c.sw.tiles, c.t0 + c.left);
+    };
+    auto next_unit = [&](Place& c) -> bool {  // false at the stretch's end
+        c.left -= c.t1 - c.t0;
+        if (c.left <= 0) return false;
+        c.t0 = 0;
+        if (++c.u == c.sw.units) {
+            c.u = 0;
+            do c.sw = seq_work<NT, SPARSE>(p, ++c.b);
+            while ((int64_t)c.sw.units * c.sw.tiles == 0 && c.b + 1 < B);
+        }
+        settle(c);
+        return true;
+    };
+    Place pl;
+    pl.sw = seq_work<NT, SPARSE>(p, b);
+    pl.b = b;
+    pl.u = u;
+    pl.t0 = t0;
+    pl.left = stretch;
+    settle(pl);
+
+    // The copies' side of this warp, up to ST tiles ahead: its next tile, whose block is looked
+    // up one issue before it is needed.
+    const int tpb = p.c.bs / 16;
+    Place ah = pl;
+    int ah_tile = ah.t0 + warp, ah_blk = -1, ah_lb = -1;
+    bool ah_more = true;
+    int ist = 0;  // the stage the next copies go to
+    auto look_up = [&]() {  // ah_tile may lie past its unit: on to the next ones
+        while (ah_tile >= ah.t1) {
+            if (!next_unit(ah)) {
+                ah_more = false;
+                return;
+            }
+            ah_tile = ah.t0 + warp;
+        }
+        const int e = ah_tile / tpb;
+        ah_lb = SPARSE ? __ldg(p.a.sel + (((int64_t)ah.b * p.t.T + ah.part) * p.c.nkv + ah.g) * p.a.n_sel + e) : e;
+        ah_blk = ah_lb < 0 ? -1 : table_block(p.t, p.c.num_blocks, ah.b, ah_lb);
+    };
+    auto issue = [&]() {
+        if (!ah_more) return;
+        const int at = warp * ST + ist;
+        if (lane == 0) {
+            const int lim = SPARSE ? ah.sw.len - ah.sw.q + ah.part + 1 : ah.sw.len;
+            const int row = ah_tile % tpb * 16;
+            const int64_t pos0 = (int64_t)ah_lb * p.c.bs + row;
+            const bool seen = ah_lb >= 0 && pos0 < lim;
+            if (seen && ah_blk < 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
+            const bool read = seen && ah_blk >= 0 && !*abort;
+            info[at].pos0 = read ? (int)pos0 : -1;
+            if (read) {
+                uint8_t* kd = ring + (size_t)at * 2 * S::kTile;
+                const int64_t sc = (int64_t)ah_blk * p.c.nkv + ah.g;
+                mbar_arrive_expect_tx(&full[at], 2 * S::kTile);
+#pragma unroll
+                for (int x = 0; x < HD; x += 128) {
+                    load_tile(kd + x * 16, &kmap, x, row, ah.g, ah_blk, &full[at]);
+                    load_tile(kd + S::kTile + x * 16, &vmap, x, row, ah.g, ah_blk, &full[at]);
+                }
+                copy4_async(&info[at].ks, p.c.k_scale + sc);
+                copy4_async(&info[at].vs, p.c.v_scale + sc);
+                copies_arrive(&full[at]);
+            } else {
+                mbar_arrive(&full[at]);
+                mbar_arrive(&full[at]);
+            }
+        }
+        if (++ist == ST) ist = 0;
+        ah_tile += kWarps;
+        look_up();
+    };
+    look_up();
+#pragma unroll 1
+    for (int i = 0; i < ST; ++i) issue();
+
+    const int gid = lane >> 2, tig = lane & 3;
+    int st = 0;
+    uint32_t ph = 0;
+    bool first = true;  // this CTA's first unit
+    do {
+        const SeqWork& sw = pl.sw;
+        const int b = pl.b, g = pl.g, part = pl.part, t0 = pl.t0, t1 = pl.t1;
+        // rows of this unit: row r is token tok, head i of the group, r_abs = tok group + i
+        const int row0 = SPARSE ? part * p.group : part * R;
+        const int nrows = SPARSE ? p.group : min(R, sw.q * p.group - row0);
+        const int tok0 = row0 / p.group;
+        const int lim0 = sw.len - sw.q + tok0 + 1;        // the fewest positions a row sees
+        const int vlim = SPARSE ? lim0 : sw.len;          // rows from here on hold nothing
+        if (!SPARSE && tid == 0 && t1 == sw.tiles && (sw.len - 1) / p.c.bs >= p.t.n_table)
+            raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);  // positions past the table
+        if (t0 == 0 && tid == 0) p.unit_base[unit_index<SPARSE>(p, b, g, part)] = beg + (stretch - pl.left);
+
+        __syncthreads();  // the previous unit's rows and sums are no longer needed
+        {
+            // q rows in f16, each scaled by 2^e so that its largest |q| lies in [2^14, 2^15)
+            constexpr int LH = HD / 8, HPL = 32 / LH;  // lanes per row, rows per warp at a time
+            for (int r = warp * HPL + lane / LH; r < R; r += kWarps * HPL) {
+                const bool has = r < nrows;
+                const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (has)
+                    v = *reinterpret_cast<const uint4*>(p.a.q + ((int64_t)b * p.t.T + tok) * p.a.q_stride +
+                                                        ((int64_t)g * p.group + i) * HD + 8 * (lane % LH));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                float mx = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+#pragma unroll
+                for (int o = LH / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const bool fin = mx < INFINITY;
+                const int e = mx > 0.f && fin ? 14 - ilogbf(mx) : 0;
+                uint32_t o4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o4[k] = pack_f16x2(ldexpf(bf16_lo(w[k]), e), ldexpf(bf16_hi(w[k]), e));
+                *reinterpret_cast<uint4*>(qh + r * QP + 8 * (lane % LH)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                if (lane % LH == 0) {
+                    hfac[r] = !has ? 0.f : fin ? ldexpf(p.a.scale * kLog2e, -e) : __uint_as_float(0x7fc00000u);
+                    lims[r] = has ? sw.len - sw.q + tok + 1 : 0x7fffffff;
+                }
+            }
+        }
+        __syncthreads();
+        uint2 qf[NT == 1 ? KC : 1];
+        if (NT == 1)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) qf[c] = *reinterpret_cast<const uint2*>(qh + gid * QP + 16 * c + 4 * tig);
+        float hf[NT][2], mr[NT][2], l[NT][2], lt[NT][2], acc[DT][NT][4];
+        float vcur = 0.f, vmax = 0.f;  // the accumulators' unit, the largest v_scale so far
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                hf[j][e] = hfac[8 * j + 2 * tig + e];
+                mr[j][e] = -INFINITY;
+                l[j][e] = lt[j][e] = 0.f;
+            }
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[dt][j][k] = 0.f;
+        }
+
+        for (int tile = t0 + warp; tile < t1; tile += kWarps) {
+            const int at = warp * ST + st;
+            if (!mbar_wait_bounded(&full[at], ph, abort) && lane == 0) raise_flag(p.t.dev_err, DEVFLAG_TIMEOUT);
+            const int pos0 = info[at].pos0;
+            const uint8_t* ks = ring + (size_t)at * 2 * S::kTile;
+            const uint8_t* vs = ks + S::kTile;
+            if (pos0 >= 0) {
+                const float kscale = info[at].ks, vscale = info[at].vs;
+                // scores of 16 positions (rows) and the unit's query rows (columns). The K
+                // dimension is permuted alike in both operands: a thread's four bytes of a
+                // 16-dim chunk are its k indices 2t, 2t + 1, 2t + 8, 2t + 9
+                float sc[NT][4];
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[j][k] = 0.f;
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(ks + chunk_at<HD>(gid, c) + 4 * tig);
+                    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(ks + chunk_at<HD>(gid + 8, c) + 4 * tig);
+                    const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)(w0 & 0xFFFFu));
+                    const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)(w0 >> 16));
+                    const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)(w1 & 0xFFFFu));
+                    const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)(w1 >> 16));
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint2 q2 = NT == 1 ? qf[c] : *reinterpret_cast<const uint2*>(qh + (8 * j + gid) * QP + 16 * c + 4 * tig);
+                        mma_f16_16816(sc[j], a0, a1, a2, a3, q2.x, q2.y);
+                    }
+                }
+                // s - m; masked positions -inf
+                const bool masked = pos0 + 16 > lim0;  // (a limit per row matters)
+                float x[NT][4];
+                bool up = false;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = hf[j][e] * kscale;
+                        x[j][e] = fmaf(sc[j][e], f, -mr[j][e]);
+                        x[j][2 + e] = fmaf(sc[j][2 + e], f, -mr[j][e]);
+                        if (masked) {
+                            const int lim = lims[8 * j + 2 * tig + e];
+                            if (pos0 + gid >= lim) x[j][e] = -INFINITY;
+                            if (pos0 + gid + 8 >= lim) x[j][2 + e] = -INFINITY;
+                        }
+                        up = up || x[j][e] > kRaise || x[j][2 + e] > kRaise;
+                    }
+                float ratio = 1.f, wmul = 1.f;
+                if (vscale != vcur) {
+                    // units: the block's v_scale, but never more than 2^90 below the largest so
+                    // far (the sums would overflow); a zero scale keeps the unit, weighs nothing
+                    if (vscale == 0.f) {
+                        wmul = 0.f;
+                    } else {
+                        vmax = fmaxf(vmax, vscale);
+                        const float unit = fmaxf(vscale, vmax * 8.077935669463161e-28f);
+                        wmul = vscale / unit;
+                        ratio = vcur / unit;
+                        vcur = unit;
+                    }
+                }
+                if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float f = hf[j][e] * kscale;
+                            const bool m0 = x[j][e] == -INFINITY, m1 = x[j][2 + e] == -INFINITY;
+                            float m = fmaxf(m0 ? -INFINITY : sc[j][e] * f, m1 ? -INFINITY : sc[j][2 + e] * f);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            const float mn = fmaxf(mr[j][e], m);
+                            const float al = mr[j][e] == -INFINITY ? 0.f : ex2(mr[j][e] - mn);
+                            mr[j][e] = mn;
+                            l[j][e] *= al;
+                            lt[j][e] *= al;
+                            x[j][e] = m0 ? -INFINITY : fmaf(sc[j][e], f, -mn);
+                            x[j][2 + e] = m1 ? -INFINITY : fmaf(sc[j][2 + e], f, -mn);
+                            const float by = al * ratio;
+#pragma unroll
+                            for (int dt = 0; dt < DT; ++dt) {
+                                acc[dt][j][e] *= by;
+                                acc[dt][j][2 + e] *= by;
+                            }
+                        }
+                } else if (ratio != 1.f) {
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) acc[dt][j][k] *= ratio;
+                }
+                // weights, rounded to f16 for the product and the denominator alike (lt: as they
+                // are), packed per position and transposed into the V product's B fragments
+                uint32_t bp[NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint16_t wl[2], wh[2];
+                    float ts[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float w0 = ex2(x[j][e]), w1 = ex2(x[j][2 + e]);
+                        uint32_t hw = pack_f16x2(w0, w1);
+                        const float2 wf = f16x2_to_f32x2(hw);
+                        ts[e] = w0 + w1;
+                        l[j][e] += wf.x + wf.y;
+                        lt[j][e] += ts[e];
+                        if (wmul != 1.f) hw = pack_f16x2(w0 * wmul, w1 * wmul);
+                        wl[e] = (uint16_t)(hw & 0xFFFFu);
+                        wh[e] = (uint16_t)(hw >> 16);
+                    }
+                    bp[j][0] = transpose8((uint32_t)wl[0] | ((uint32_t)wl[1] << 16));
+                    bp[j][1] = transpose8((uint32_t)wh[0] | ((uint32_t)wh[1] << 16));
+                    if (!SPARSE && p.a.out_mass) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float s = ts[e];
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                            const int r = 8 * j + 2 * tig + e;
+                            if (gid == 0 && r < nrows) {
+                                const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
+                                p.tile_lse[(((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i) * p.tiles + tile] =
+                                    s > 0.f ? mr[j][e] + log2f(s) : s != s ? s : -INFINITY;
+                            }
+                        }
+                    }
+                }
+                // V^T (A) . W^T (B) over 16 positions. Tile 2 mp + u2 has dim 32 mp + 4 gid + 2 u2
+                // in row gid and the next in row gid + 8, so that a thread's dims are one word per
+                // position. In a masked tile, rows past the end are zeroed (0 * NaN is NaN) and
+                // NaN codes taken out, to be given back to the rows that see them.
+                const int pr = 2 * tig;
+                bool nan_any = false;
+                if (masked) {
+#pragma unroll
+                    for (int mp = 0; mp < HD / 32; ++mp) {
+                        const int vc = 2 * mp + (gid >> 2), vo = 4 * (gid & 3);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = pr + (k & 1) + 8 * (k >> 1);
+                            uint32_t* y = const_cast<uint32_t*>(reinterpret_cast<const uint32_t*>(vs + chunk_at<HD>(r, vc) + vo));
+                            if (pos0 + r >= vlim) *y = 0;  // (each word of V belongs to one lane)
+                            else nan_any = nan_any || __vcmpeq4(*y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        }
+                    }
+                    nan_any = __any_sync(0xffffffffu, nan_any);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the copies that follow
+                }
+#pragma unroll
+                for (int mp = 0; mp < HD / 32; ++mp) {
+                    const int vc = 2 * mp + (gid >> 2), vo = 4 * (gid & 3);
+                    uint32_t y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = *reinterpret_cast<const uint32_t*>(vs + chunk_at<HD>(pr + (k & 1) + 8 * (k >> 1), vc) + vo);
+                    int nan_at[4];  // first position with a NaN, for each of the four dims
+                    if (nan_any) {
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) nan_at[d] = 0x7fffffff;
+#pragma unroll
+                        for (int k = 3; k >= 0; --k) {
+                            const uint32_t isn = __vcmpeq4(y[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+                            for (int d = 0; d < 4; ++d)
+                                if ((isn >> (8 * d)) & 1u) nan_at[d] = min(nan_at[d], pos0 + pr + (k & 1) + 8 * (k >> 1));
+                            y[k] &= ~isn;
+                        }
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            nan_at[d] = min(nan_at[d], __shfl_xor_sync(0xffffffffu, nan_at[d], 1));
+                            nan_at[d] = min(nan_at[d], __shfl_xor_sync(0xffffffffu, nan_at[d], 2));
+                        }
+                    }
+#pragma unroll
+                    for (int u2 = 0; u2 < 2; ++u2) {
+                        const uint32_t s0 = 0x0040u + 0x0022u * u2, s1 = s0 + 0x0011u;
+                        const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[0], y[1], s0));
+                        const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[0], y[1], s1));
+                        const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[2], y[3], s0));
+                        const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[2], y[3], s1));
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            mma_f16_16816(acc[2 * mp + u2][j], a0, a1, a2, a3, bp[j][0], bp[j][1]);
+                            if (nan_any)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int lim = lims[8 * j + 2 * tig + e];
+                                    if (nan_at[2 * u2] < lim) acc[2 * mp + u2][j][e] = __uint_as_float(0x7fc00000u);
+                                    if (nan_at[2 * u2 + 1] < lim) acc[2 * mp + u2][j][2 + e] = __uint_as_float(0x7fc00000u);
+                                }
+                        }
+                    }
+                }
+            } else if (!SPARSE && p.a.out_mass) {
+                for (int r = lane; r < nrows; r += 32) {
+                    const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
+                    p.tile_lse[(((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i) * p.tiles + tile] = -INFINITY;
+                }
+            }
+            __syncwarp();  // everyone is done with the stage
+            issue();
+            if (++st == ST) {
+                st = 0;
+                ph ^= 1;
+            }
+        }
+
+        // join the four warps (fixed order): the largest reference M, everything times 2^(m - M)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], o);
+                    lt[j][e] += __shfl_xor_sync(0xffffffffu, lt[j][e], o);
+                }
+        if (gid == 0)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = warp * R + 8 * j + 2 * tig + e;
+                    redm[r] = mr[j][e];
+                    redl[r] = l[j][e];
+                    redt[r] = lt[j][e];
+                }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * j + 2 * tig + e;
+                float M = redm[r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) M = fmaxf(M, redm[w * R + r]);
+                const float mine = mr[j][e] == -INFINITY ? 0.f : ex2(mr[j][e] - M);
+                float L = 0.f, Lt = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = redm[w * R + r] == -INFINITY ? 0.f : ex2(redm[w * R + r] - M);
+                    L += f * redl[w * R + r];
+                    Lt += f * redt[w * R + r];
+                }
+                mr[j][e] = M;
+                l[j][e] = L;
+                lt[j][e] = Lt;
+                const float by = mine * vcur;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    acc[dt][j][e] *= by;
+                    acc[dt][j][2 + e] *= by;
+                }
+            }
+        // warps 2 and 3 hand theirs to 0 and 1, then 1 to 0
+#pragma unroll
+        for (int half = kWarps / 2; half; half >>= 1) {
+            if (warp >= half && warp < 2 * half) {
+                float4* to = xacc + (size_t)(half == 2 ? warp - half : 1) * DT * NT * 32;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        to[(dt * NT + j) * 32 + lane] = make_float4(acc[dt][j][0], acc[dt][j][1], acc[dt][j][2], acc[dt][j][3]);
+            }
+            __syncthreads();
+            if (warp < half) {
+                const float4* from = xacc + (size_t)(half == 2 ? warp : 1) * DT * NT * 32;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float4 v = from[(dt * NT + j) * 32 + lane];
+                        acc[dt][j][0] += v.x;
+                        acc[dt][j][1] += v.y;
+                        acc[dt][j][2] += v.z;
+                        acc[dt][j][3] += v.w;
+                    }
+            }
+        }
+        if (warp == 0) {
+            const bool whole = t0 == 0 && t1 == sw.tiles;
+            float* slot = p.parts + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * (R * (HD + 4));
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * j + 2 * tig + e;
+                    if (r >= nrows) continue;
+                    const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
+                    const int64_t row = ((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i;
+                    const bool some = !(l[j][e] <= 0.f);
+                    const float inv = some ? 1.f / l[j][e] : 0.f;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt) {
+                        const int d = 32 * (dt / 2) + 4 * gid + 2 * (dt % 2);
+                        if (whole)
+                            *reinterpret_cast<uint32_t*>(p.a.out + row * HD + d) =
+                                some ? f32x2_to_bf16x2(acc[dt][j][e] * inv, acc[dt][j][2 + e] * inv) : 0u;
+                        else
+                            *reinterpret_cast<float2*>(slot + R * 4 + r * HD + d) = make_float2(acc[dt][j][e], acc[dt][j][2 + e]);
+                    }
+                    if (gid == 0) {
+                        if (whole) {
+                            const float lse2 = some ? mr[j][e] + log2f(lt[j][e]) : -INFINITY;
+                            if (p.a.out_lse) p.a.out_lse[row] = lse2 * kLn2;
+                            if (!SPARSE && p.a.out_mass) p.row_lse[row] = lse2;
+                        } else {
+                            slot[r] = mr[j][e];
+                            slot[R + r] = l[j][e];
+                            slot[2 * R + r] = lt[j][e];
+                        }
+                    }
+                }
+        }
+        first = false;
+    } while (next_unit(pl));
+    // after a timeout: wait (again with a limit) for the copies that are still in flight
+    if (*abort && lane == 0)
+        for (int s = 0; s < ST; ++s) mbar_wait_bounded(&full[warp * ST + s], ph ^ (s < st ? 1u : 0u), nullptr, kWaitLimitCycles / 8);
+}
+
+// Joins the partial sums of the units that several CTAs share, and writes the rows that see
+// nothing. One warp or four (they split the parts) per query row.
+template <int HD, int NT, bool SPARSE, int WPR>
+__global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int R = 8 * NT, V = HD / 32;
+    __shared__ float sums[4][HD];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + warp;
+    const int wr = WPR == 4 ? warp : 0;
+    pdl_wait();
+    const int64_t bt = row / p.a.nq;
+    const int b = (int)(bt / p.t.T), tok = (int)(bt % p.t.T), head = (int)(row % p.a.nq);
+    if (b >= p.t.B) return;
+    const SeqWork sw = seq_work<NT, SPARSE>(p, b);
+    if (tok >= sw.q) return;
+    const int g = head / p.group;
+    const int r_abs = SPARSE ? head - g * p.group : tok * p.group + head - g * p.group;
+    const int part = SPARSE ? tok : r_abs / R, r = SPARSE ? r_abs : r_abs - part * R;
+    float M = -INFINITY, L = 0.f, Lt = 0.f, a[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = 0.f;
+    if (sw.tiles > 0) {
+        const int64_t per = *p.per, base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
+        const int64_t c0 = base / per, c1 = (base + sw.tiles - 1) / per;
+        if (c0 == c1) return;  // finished by one CTA
+        const float* parts = p.parts;
+        // in CTA c0 the unit is the last (slot 1) unless it is also the first; in later ones the first
+        auto slot = [&](int64_t c) {
+            return parts + (c * 2 + (c == c0 && base != c0 * per ? 1 : 0)) * (int64_t)(R * (HD + 4));
+        };
+        for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[r]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int64_t c = c0 + lane; c <= c1; c += 32) {
+            const float* s = slot(c);
+            const float f = s[r] == -INFINITY ? 0.f : ex2(s[r] - M);
+            L += f * s[R + r];
+            Lt += f * s[2 * R + r];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, o);
+            Lt += __shfl_xor_sync(0xffffffffu, Lt, o);
+        }
+#pragma unroll 4
+        for (int64_t c = c0 + wr; c <= c1; c += WPR) {
+            const float* s = slot(c);
+            const float f = s[r] == -INFINITY ? 0.f : ex2(s[r] - M);
+            const float* x = s + R * 4 + r * HD + lane * V;
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[v] = fmaf(f, x[v], a[v]);
+        }
+        if (WPR == 4) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) sums[warp][lane * V + v] = a[v];
+            __syncthreads();  // (every warp of the CTA has the same row)
+            if (warp) return;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                a[v] = ((a[v] + sums[1][lane * V + v]) + sums[2][lane * V + v]) + sums[3][lane * V + v];
+        }
+    } else if (WPR == 4 && warp) {
+        return;
+    }
+    const bool some = !(L <= 0.f);
+    const float inv = some ? 1.f / L : 0.f;
+    uint16_t* out = p.a.out + row * HD + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+        *reinterpret_cast<uint32_t*>(out + v) = some ? f32x2_to_bf16x2(a[v] * inv, a[v + 1] * inv) : 0u;
     if (lane == 0) {
-        const float lse2 = l > 0.f || l != l ? m + log2f(l) : -INFINITY;
-        if (p.a.out_lse) p.a.out_lse[bt * p.a.nq + i] = lse2 * kLn2;
-        if (p.a.out_mass) p.row_lse[bt * p.a.nq + i] = lse2;
+        const float lse2 = some ? M + log2f(Lt) : -INFINITY;
+        if (p.a.out_lse) p.a.out_lse[row] = lse2 * kLn2;
+        if (!SPARSE && p.a.out_mass) p.row_lse[row] = lse2;
     }
 }
 
@@ -89,55 +792,155 @@ __global__ void __launch_bounds__(128) block_attn_simple_kernel(const __grid_con
 __global__ void __launch_bounds__(128) block_mass_kernel(const __grid_constant__ AttnParams p) {
     const int b = blockIdx.y;
     const int64_t j = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    pdl_wait();
     if (j >= p.t.n_table) return;
     const SeqStep s = seq_step(p.t, b);
     const int tpb = p.c.bs / 16;
     const int64_t at = (int64_t)b * p.t.n_table + j;
+    const int ntiles = (int)min((int64_t)tpb, (s.len + 15) / 16 - j * tpb);
     float sum = 0.f;
-    for (int tok = 0; tok < s.q; ++tok) {
-        if (j >= blocks_of(s.len - s.q + tok + 1, p.c.bs, p.t.n_table)) continue;
-        for (int i = 0; i < p.a.nq; ++i) {
-            const int64_t row = ((int64_t)b * p.t.T + tok) * p.a.nq + i;
+    if (ntiles > 0)
+        for (int64_t row = (int64_t)b * p.t.T * p.a.nq, end = row + (int64_t)s.q * p.a.nq; row < end; ++row) {
             const float L = p.row_lse[row];
-            for (int u = 0; u < tpb; ++u) {
+            for (int u = 0; u < ntiles; ++u) {
                 const float x = p.tile_lse[row * p.tiles + j * tpb + u];
                 if (x != -INFINITY) sum += exp2f(x - L);
             }
         }
-    }
     p.a.out_mass[at] = (p.a.mass ? p.a.mass[at] : 0.f) + sum;
 }
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// Row tiles of 8 NT query rows: the smallest that holds them, 32 rows at most (16 for 256-dim
+// heads, whose accumulators are twice as long).
+int pick_nt(int hd, int64_t rows) { return rows <= 8 ? 1 : rows <= 16 || hd == 256 ? 2 : 4; }
+
+struct Layout {
+    int nt, row_tiles;
+    int64_t units, tiles;
+    size_t base, parts, row_lse, tile_lse, bytes;  // offsets
+};
+Layout layout_of(const BlockCache& c, int B, int64_t T, int nq, int64_t n_table, bool sparse, bool mass) {
+    Layout l{};
+    const int64_t rows = (sparse ? 1 : T) * (nq / c.nkv);
+    l.nt = pick_nt(c.hd, rows);
+    l.row_tiles = (int)((rows + 8 * l.nt - 1) / (8 * l.nt));
+    l.units = (int64_t)B * c.nkv * (sparse ? T : l.row_tiles);
+    l.tiles = n_table * (c.bs / 16);
+    l.base = 16;
+    l.parts = l.base + up16((size_t)l.units * 8);
+    l.row_lse = l.parts + (size_t)2 * kMaxGrid * 8 * l.nt * (c.hd + 4) * 4;
+    const size_t q_rows = (size_t)B * T * nq;
+    l.tile_lse = l.row_lse + (mass ? up16(q_rows * 4) : 0);
+    l.bytes = l.tile_lse + (mass ? up16(q_rows * 4 * (size_t)l.tiles) : 0);
+    return l;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(f);
+    });
+    return fn;
+}
+
+// The cache's codes as a 4-D tensor (byte of the row, row of the block, head, block), in boxes
+// of 16 rows of at most 128 bytes.
+bool cache_map(CUtensorMap* m, const BlockCache& c, const uint8_t* base) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)c.hd, (cuuint64_t)c.bs, (cuuint64_t)c.nkv, (cuuint64_t)c.num_blocks};
+    cuuint64_t strides[3] = {(cuuint64_t)c.row_stride, (cuuint64_t)c.head_stride, (cuuint64_t)c.block_stride};
+    cuuint32_t box[4] = {(cuuint32_t)(c.hd < 128 ? c.hd : 128), 16, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, c.hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launches `kern` so that it may start while the kernel before it in the stream ends (each of
+// ours waits for that before it touches memory).
+template <class K, class... A>
+cudaError_t launch_after(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int HD, int NT, bool SPARSE>
+cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
+    using Sh = Shape<HD, NT>;
+    auto kern = block_attn_kernel<HD, NT, SPARSE>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    int grid = sms * Sh::kPerSm;
+    if (grid > kMaxGrid) grid = kMaxGrid;
+    if ((e = launch_after(kern, dim3((unsigned)grid), kThreads, Sh::kSmem, s, p, km, vm)) != cudaSuccess) return e;
+    // four warps per row while the rows are few (many parts each), one when they fill the GPU
+    const int64_t rows = (int64_t)p.t.B * p.t.T * p.a.nq;
+    if (rows <= 4096) return launch_after(block_attn_join_kernel<HD, NT, SPARSE, 4>, dim3((unsigned)rows), 128, 0, s, p);
+    return launch_after(block_attn_join_kernel<HD, NT, SPARSE, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, p);
+}
+
+template <int HD, bool SPARSE>
+cudaError_t launch_attn_nt(int nt, const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
+    if (nt == 1) return launch_attn<HD, 1, SPARSE>(p, km, vm, sms, s);
+    if constexpr (HD < 256 && !SPARSE)
+        if (nt == 4) return launch_attn<HD, 4, SPARSE>(p, km, vm, sms, s);
+    return launch_attn<HD, 2, SPARSE>(p, km, vm, sms, s);
+}
+
+template <int HD>
+cudaError_t launch_attn_hd(int nt, const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
+    return p.a.sel ? launch_attn_nt<HD, true>(nt, p, km, vm, sms, s) : launch_attn_nt<HD, false>(nt, p, km, vm, sms, s);
+}
 
 }  // namespace
 
 int block_attn_max_group() { return kMaxGroup; }
 int block_attn_max_t() { return kMaxT; }
 
-size_t block_attn_ws_bytes(const BlockCache& c, int B, int T, int nq, int64_t n_table, int n_sel,
-                           bool sparse, bool mass) {
-    (void)n_sel;
-    (void)sparse;
-    const size_t rows = (size_t)B * T * nq;
-    return 16 + (mass ? up16(rows * 4) + up16(rows * 4 * (size_t)(n_table * c.bs / 16)) : 0);
+size_t block_attn_ws_bytes(const BlockCache& c, int B, int T, int nq, int64_t n_table, bool sparse, bool mass) {
+    return layout_of(c, B, T, nq, n_table, sparse, mass).bytes;
 }
 
 cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const BlockAttnArgs& a,
                               cudaStream_t s) {
-    const int64_t rows = (int64_t)t.B * t.T * a.nq;
-    if (rows / 4 >= INT32_MAX) return cudaErrorInvalidValue;
-    AttnParams p{c, t, a, a.nq / c.nkv, (int)(t.n_table * c.bs / 16), nullptr, nullptr};
-    p.row_lse = static_cast<float*>(a.ws);
-    p.tile_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + up16((size_t)rows * 4));
-    const unsigned grid = (unsigned)((rows + 3) / 4);
-    if (c.hd == 64) block_attn_simple_kernel<64><<<grid, 128, 0, s>>>(p);
-    else if (c.hd == 128) block_attn_simple_kernel<128><<<grid, 128, 0, s>>>(p);
-    else block_attn_simple_kernel<256><<<grid, 128, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const bool sparse = a.sel != nullptr;
+    const Layout l = layout_of(c, t.B, t.T, a.nq, t.n_table, sparse, a.out_mass != nullptr);
+    if ((int64_t)t.B * t.T * a.nq > INT32_MAX) return cudaErrorInvalidValue;
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    AttnParams p{c, t, a, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int64_t*>(ws),
+                 reinterpret_cast<int64_t*>(ws + l.base), reinterpret_cast<float*>(ws + l.parts),
+                 reinterpret_cast<float*>(ws + l.row_lse), reinterpret_cast<float*>(ws + l.tile_lse)};
+    int dev = 0, sms = 148;
+    cudaError_t e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    CUtensorMap km{}, vm{};
+    if (!cache_map(&km, c, c.k) || !cache_map(&vm, c, c.v)) return cudaErrorInvalidValue;
+    e = c.hd == 64 ? launch_attn_hd<64>(l.nt, p, km, vm, sms, s)
+                   : c.hd == 128 ? launch_attn_hd<128>(l.nt, p, km, vm, sms, s) : launch_attn_hd<256>(l.nt, p, km, vm, sms, s);
     if (e != cudaSuccess || !a.out_mass) return e;
-    block_mass_kernel<<<dim3((unsigned)((t.n_table + 127) / 128), (unsigned)t.B), 128, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(block_mass_kernel, dim3((unsigned)((t.n_table + 127) / 128), (unsigned)t.B), 128, 0, s, p);
 }
 
 }  // namespace mtp

@@ -202,8 +202,8 @@ struct BlockAttnArgs {
 };
 int block_attn_max_group();
 int block_attn_max_t();
-size_t block_attn_ws_bytes(const BlockCache& c, int B, int T, int nq, int64_t n_table, int n_sel,
-                           bool sparse, bool mass);
+size_t block_attn_ws_bytes(const BlockCache& c, int B, int T, int nq, int64_t n_table, bool sparse,
+                           bool mass);
 cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const BlockAttnArgs& a,
                               cudaStream_t s);
 size_t block_select_ws_bytes(const BlockCache& c, int B, int T, int64_t n_table);
