@@ -51,11 +51,12 @@ struct AttnParams {
     int group;
     int row_tiles;       // dense: row tiles of 8 NT rows that T tokens have at most
     int64_t tiles;       // 16-position tiles of n_table blocks (tile_lse's pitch)
-    int64_t* per;        // [1] tiles per CTA
-    int64_t* unit_base;  // [units] first tile of each unit on the line
+    int32_t* per;        // [1] tiles per CTA
+    int32_t* unit_base;  // [units] first tile of each unit on the line
+    int tile_shift;      // log2(16-position tiles per block)
     float* parts;        // [2 kMaxGrid][8 NT (hd + 4)] partial sums of a CTA's first and last unit
-    float* row_lse;      // [B, T, nq] base-2 log-sum-exp (with mass)
-    float* tile_lse;     // [B, T, nq, tiles] (with mass)
+    float* row_lse;      // [B, nkv, T group] base-2 log-sum-exp (with mass)
+    float* tile_lse;     // [B, nkv, tiles, T group] of each tile's positions (with mass)
 };
 
 // A sequence's units and the tiles each has.
@@ -68,11 +69,11 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
     SeqWork w{s.len, s.q, 0, 0};
     if (SPARSE) {
         w.units = s.q * p.c.nkv;
-        w.tiles = s.len > 0 ? p.a.n_sel * (p.c.bs / 16) : 0;
+        w.tiles = s.len > 0 ? p.a.n_sel << p.tile_shift : 0;
     } else {
         w.units = p.c.nkv * ((s.q * p.group + 8 * NT - 1) / (8 * NT));
         const int nb = blocks_of(s.len, p.c.bs, p.t.n_table);
-        w.tiles = min((s.len + 15) / 16, nb * (p.c.bs / 16));
+        w.tiles = min((s.len >> 4) + ((s.len & 15) != 0), nb << p.tile_shift);
     }
     return w;
 }
@@ -92,7 +93,7 @@ struct Shape {
     static constexpr size_t kFixed = (size_t)HD * NT * 64         // two warps' accumulators
                                      + (size_t)kRows * kQPitch * 2  // q
                                      + (size_t)kRows * 8            // score factors, limits
-                                     + (size_t)3 * kWarps * kRows * 4 + 16;
+                                     + (size_t)2 * kWarps * kRows * 4 + 16;
     static constexpr size_t kStage = (size_t)kWarps * (2 * kTile + 16 + 8);  // tiles, info, barriers
     // (1 KB of each CTA's share of the SM's 228 KB is the system's)
     static constexpr int kStages = (int)(((size_t)(228 * 1024) / kPerSm - 1024 - kFixed) / kStage);
@@ -138,12 +139,43 @@ __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, int
         : "memory");
 }
 
-// Byte offset of 16-byte chunk c of row r in a stage's K or V tile, as the swizzled tensor
-// copies leave it: rows of 128 bytes (64 for hd = 64; hd = 256: two halves of 128).
+// How a warp reads a stage's tile (rows of 128 bytes whose 16-byte chunks are swizzled by
+// chunk ^ (row & 7); hd = 64: rows of 64 bytes, chunk ^ ((row / 2) & 3); hd = 256: two halves
+// of 128 columns). Lane 4 gid + tig reads 16 bytes at a time, without bank conflicts because
+// the tile's positions and columns are permuted, which no sum notices: MMA row m is position
+// pos_of(m), and lane column group gid holds the columns col_of(gid) on.
 template <int HD>
-__device__ __forceinline__ int chunk_at(int r, int c) {
-    if (HD == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-    return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+__device__ __forceinline__ constexpr int pos_of(int m) {  // m < 8; rows 8 .. 15: 8 more
+    return HD == 64 ? m ^ ((m >> 1) & 1) : (m & 1) * 4 + (m >> 1);
+}
+template <int HD>
+__device__ __forceinline__ constexpr int col_of(int gid) {
+    return HD == 64 ? 8 * gid : 16 * ((gid >> 1) + 4 * (gid & 1));
+}
+template <int HD>
+__device__ __forceinline__ uint32_t swizzled(int row, int byte) {  // row < 16, byte < min(HD, 128)
+    return HD == 64 ? row * 64 + (byte ^ (((row >> 1) & 3) << 4)) : row * 128 + (byte ^ ((row & 7) << 4));
+}
+// Offset of what lane column group gid reads of MMA row m of V (its first half of 256 columns).
+template <int HD>
+__device__ __forceinline__ uint32_t S_voff(int m, int gid) {
+    return HD == 64 ? swizzled<HD>(pos_of<HD>(m), col_of<HD>(gid) & ~15) + (col_of<HD>(gid) & 15)
+                    : swizzled<HD>(pos_of<HD>(m), col_of<HD>(gid));
+}
+__device__ __forceinline__ uint4 lds4(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds2(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+
+// The slow part of a wait, kept out of the tile loop's code.
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* dev_err) {
+    if (!mbar_wait_bounded(bar, parity, abort)) raise_flag(dev_err, DEVFLAG_TIMEOUT);
 }
 
 template <int HD, int NT, bool SPARSE>
@@ -162,8 +194,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     int* lims = reinterpret_cast<int*>(hfac + R);                                        // [R]
     float* redm = reinterpret_cast<float*>(lims + R);                                    // [warp][R]
     float* redl = redm + kWarps * R;
-    float* redt = redl + kWarps * R;
-    volatile int* abort = reinterpret_cast<volatile int*>(redt + kWarps * R);
+    volatile int* abort = reinterpret_cast<volatile int*>(redl + kWarps * R);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
@@ -180,47 +211,40 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     // this CTA's stretch of the line: [beg, end), its first sequence, unit and tile (every warp
     // for itself: two passes over the lengths, 32 sequences at a time)
     const int B = p.t.B;
-    int64_t total = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-        int64_t n = 0;
+    int total = 0;
+    for (int b0 = 0; b0 < B; b0 += 32)
         if (b0 + lane < B) {
             const SeqWork w = seq_work<NT, SPARSE>(p, b0 + lane);
-            n = (int64_t)w.units * w.tiles;
+            total += w.units * w.tiles;
         }
-        total += n;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    per = (per + kWarps - 1) / kWarps * kWarps;
+    total = __reduce_add_sync(0xffffffffu, total);
+    const int grid = (int)gridDim.x;
+    const int per = (total / grid + (total % grid != 0) + kWarps - 1) / kWarps * kWarps;
     if (blockIdx.x == 0 && tid == 0) *p.per = per;
-    const int64_t beg = (int64_t)blockIdx.x * per;
-    const int64_t stretch = min(total, beg + per) - beg;
-    if (stretch <= 0) return;
+    if ((int64_t)blockIdx.x * per >= total) return;
+    const int beg = (int)blockIdx.x * per;
+    const int stretch = min(total - beg, per);
     int b = 0, u = 0, t0 = 0;
     {
-        int64_t before = 0;
+        int before = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
-            int64_t n = 0;
             SeqWork w{0, 0, 0, 0};
-            if (b0 + lane < B) {
-                w = seq_work<NT, SPARSE>(p, b0 + lane);
-                n = (int64_t)w.units * w.tiles;
-            }
-            int64_t inc = n;
+            if (b0 + lane < B) w = seq_work<NT, SPARSE>(p, b0 + lane);
+            const int n = w.units * w.tiles;
+            int inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += v;
             }
             const uint32_t past = __ballot_sync(0xffffffffu, before + inc > beg);
             if (past) {
                 const int src = __ffs(past) - 1;
-                const int64_t off = beg - (before + __shfl_sync(0xffffffffu, inc - n, src));
+                const int off = beg - (before + __shfl_sync(0xffffffffu, inc - n, src));
                 const int tiles = __shfl_sync(0xffffffffu, w.tiles, src);
                 b = b0 + src;
-                u = (int)(off / tiles);
-                t0 = (int)(off - (int64_t)u * tiles);
+                u = off / tiles;
+                t0 = off - u * tiles;
                 break;
             }
             before += __shfl_sync(0xffffffffu, inc, 31);
@@ -231,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     struct Place {
         SeqWork sw;
         int b, u, g, part, t0, t1;
-        int64_t left;  // tiles of the stretch from t0 on
+        int left;  // tiles of the stretch from t0 on
     };
     auto settle = [&](Place& c) {
         if (SPARSE) {
@@ -242,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             c.g = c.u / rt;
             c.part = c.u - c.g * rt;
         }
-        c.t1 = (int)min((int64_t)c.sw.tiles, c.t0 + c.left);
+        c.t1 = min(c.sw.tiles, c.t0 + c.left);
     };
     auto next_unit = [&](Place& c) -> bool {  // false at the stretch's end
         c.left -= c.t1 - c.t0;
@@ -251,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         if (++c.u == c.sw.units) {
             c.u = 0;
             do c.sw = seq_work<NT, SPARSE>(p, ++c.b);
-            while ((int64_t)c.sw.units * c.sw.tiles == 0 && c.b + 1 < B);
+            while (c.sw.units * c.sw.tiles == 0 && c.b + 1 < B);
         }
         settle(c);
         return true;
@@ -266,7 +290,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 
     // The copies' side of this warp, up to ST tiles ahead: its next tile, whose block is looked
     // up one issue before it is needed.
-    const int tpb = p.c.bs / 16;
     Place ah = pl;
     int ah_tile = ah.t0 + warp, ah_blk = -1, ah_lb = -1;
     bool ah_more = true;
@@ -279,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             }
             ah_tile = ah.t0 + warp;
         }
-        const int e = ah_tile / tpb;
+        const int e = ah_tile >> p.tile_shift;
         ah_lb = SPARSE ? __ldg(p.a.sel + (((int64_t)ah.b * p.t.T + ah.part) * p.c.nkv + ah.g) * p.a.n_sel + e) : e;
         ah_blk = ah_lb < 0 ? -1 : table_block(p.t, p.c.num_blocks, ah.b, ah_lb);
     };
@@ -288,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         const int at = warp * ST + ist;
         if (lane == 0) {
             const int lim = SPARSE ? ah.sw.len - ah.sw.q + ah.part + 1 : ah.sw.len;
-            const int row = ah_tile % tpb * 16;
+            const int row = 16 * (ah_tile & ((1 << p.tile_shift) - 1));
             const int64_t pos0 = (int64_t)ah_lb * p.c.bs + row;
             const bool seen = ah_lb >= 0 && pos0 < lim;
             if (seen && ah_blk < 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
@@ -320,6 +343,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     for (int i = 0; i < ST; ++i) issue();
 
     const int gid = lane >> 2, tig = lane & 3;
+    constexpr int kPitch = HD == 64 ? 64 : 128, kWords = HD == 64 ? 2 : 4;  // of a (half) tile; words a lane holds of a V row
+    const uint32_t ring_at = smem_u32(ring);
+    const uint32_t koff = swizzled<HD>(pos_of<HD>(gid), 16 * tig);
+    const uint32_t voff0 = S_voff<HD>(2 * tig, gid), voff1 = S_voff<HD>(2 * tig + 1, gid);
     int st = 0;
     uint32_t ph = 0;
     bool first = true;  // this CTA's first unit
@@ -332,6 +359,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         const int tok0 = row0 / p.group;
         const int lim0 = sw.len - sw.q + tok0 + 1;        // the fewest positions a row sees
         const int vlim = SPARSE ? lim0 : sw.len;          // rows from here on hold nothing
+        const int mass_pitch = (int)p.t.T * p.group;  // rows of a kv head
+        float* mass_at = nullptr;
+        if (!SPARSE && p.a.out_mass) mass_at = p.tile_lse + ((int64_t)b * p.c.nkv + g) * p.tiles * mass_pitch + row0;
         if (!SPARSE && tid == 0 && t1 == sw.tiles && (sw.len - 1) / p.c.bs >= p.t.n_table)
             raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);  // positions past the table
         if (t0 == 0 && tid == 0) p.unit_base[unit_index<SPARSE>(p, b, g, part)] = beg + (stretch - pl.left);
@@ -366,11 +396,14 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             }
         }
         __syncthreads();
-        uint2 qf[NT == 1 ? KC : 1];
+        // B fragments of the scores: k-step 4 h + s of the matrix product is, in lane tig, dims
+        // 64 h + 16 tig + 4 s .. + 3 (as the K bytes of a 16-byte load come)
+        uint4 qf[NT == 1 ? KC / 2 : 1];
         if (NT == 1)
 #pragma unroll
-            for (int c = 0; c < KC; ++c) qf[c] = *reinterpret_cast<const uint2*>(qh + gid * QP + 16 * c + 4 * tig);
-        float hf[NT][2], mr[NT][2], l[NT][2], lt[NT][2], acc[DT][NT][4];
+            for (int c = 0; c < KC / 2; ++c)
+                qf[c] = *reinterpret_cast<const uint4*>(qh + gid * QP + 64 * (c >> 1) + 16 * tig + 8 * (c & 1));
+        float hf[NT][2], mr[NT][2], l[NT][2], acc[DT][NT][4];
         float vcur = 0.f, vmax = 0.f;  // the accumulators' unit, the largest v_scale so far
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -378,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             for (int e = 0; e < 2; ++e) {
                 hf[j][e] = hfac[8 * j + 2 * tig + e];
                 mr[j][e] = -INFINITY;
-                l[j][e] = lt[j][e] = 0.f;
+                l[j][e] = 0.f;
             }
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt)
@@ -388,38 +421,43 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 
         for (int tile = t0 + warp; tile < t1; tile += kWarps) {
             const int at = warp * ST + st;
-            if (!mbar_wait_bounded(&full[at], ph, abort) && lane == 0) raise_flag(p.t.dev_err, DEVFLAG_TIMEOUT);
+            if (!mbar_try_wait(&full[at], ph)) wait_long(&full[at], ph, abort, p.t.dev_err);
             const int pos0 = info[at].pos0;
-            const uint8_t* ks = ring + (size_t)at * 2 * S::kTile;
-            const uint8_t* vs = ks + S::kTile;
             if (pos0 >= 0) {
+                const uint32_t stage = ring_at + (uint32_t)at * (2 * S::kTile);
                 const float kscale = info[at].ks, vscale = info[at].vs;
-                // scores of 16 positions (rows) and the unit's query rows (columns). The K
-                // dimension is permuted alike in both operands: a thread's four bytes of a
-                // 16-dim chunk are its k indices 2t, 2t + 1, 2t + 8, 2t + 9
+                // scores of 16 positions (rows) and the unit's query rows (columns)
                 float sc[NT][4];
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sc[j][k] = 0.f;
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(ks + chunk_at<HD>(gid, c) + 4 * tig);
-                    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(ks + chunk_at<HD>(gid + 8, c) + 4 * tig);
-                    const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)(w0 & 0xFFFFu));
-                    const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)(w0 >> 16));
-                    const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)(w1 & 0xFFFFu));
-                    const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)(w1 >> 16));
+                for (int h = 0; h < HD / 64; ++h) {  // 64 dims at a time
+                    const uint32_t ka = (stage + (h >> 1) * 2048 + koff) ^ ((h & 1) << 6);
+                    const uint4 k0 = lds4(ka), k1 = lds4(ka + 8 * kPitch);
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const uint2 q2 = NT == 1 ? qf[c] : *reinterpret_cast<const uint2*>(qh + (8 * j + gid) * QP + 16 * c + 4 * tig);
-                        mma_f16_16816(sc[j], a0, a1, a2, a3, q2.x, q2.y);
+                    for (int t = 0; t < 2; ++t) {
+                        uint32_t a[2][4];
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            a[v][0] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] & 0xFFFFu));
+                            a[v][1] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] & 0xFFFFu));
+                            a[v][2] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] >> 16));
+                            a[v][3] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] >> 16));
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const uint4 q4 = NT == 1 ? qf[2 * h + t] : *reinterpret_cast<const uint4*>(qh + (8 * j + gid) * QP + 64 * h + 16 * tig + 8 * t);
+                            mma_f16_16816(sc[j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
+                            mma_f16_16816(sc[j], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
+                        }
                     }
                 }
                 // s - m; masked positions -inf
                 const bool masked = pos0 + 16 > lim0;  // (a limit per row matters)
-                float x[NT][4];
-                bool up = false;
+                float x[NT][4], top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -427,13 +465,18 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                         const float f = hf[j][e] * kscale;
                         x[j][e] = fmaf(sc[j][e], f, -mr[j][e]);
                         x[j][2 + e] = fmaf(sc[j][2 + e], f, -mr[j][e]);
-                        if (masked) {
-                            const int lim = lims[8 * j + 2 * tig + e];
-                            if (pos0 + gid >= lim) x[j][e] = -INFINITY;
-                            if (pos0 + gid + 8 >= lim) x[j][2 + e] = -INFINITY;
-                        }
-                        up = up || x[j][e] > kRaise || x[j][2 + e] > kRaise;
                     }
+                if (masked)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int lim = lims[8 * j + 2 * tig + e];
+                            if (pos0 + pos_of<HD>(gid) >= lim) x[j][e] = -INFINITY;
+                            if (pos0 + pos_of<HD>(gid) + 8 >= lim) x[j][2 + e] = -INFINITY;
+                        }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
                 float ratio = 1.f, wmul = 1.f;
                 if (vscale != vcur) {
                     // units: the block's v_scale, but never more than 2^90 below the largest so
@@ -448,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                         vcur = unit;
                     }
                 }
-                if (__any_sync(0xffffffffu, up)) {
+                if (__any_sync(0xffffffffu, top > kRaise)) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -462,7 +505,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                             const float al = mr[j][e] == -INFINITY ? 0.f : ex2(mr[j][e] - mn);
                             mr[j][e] = mn;
                             l[j][e] *= al;
-                            lt[j][e] *= al;
                             x[j][e] = m0 ? -INFINITY : fmaf(sc[j][e], f, -mn);
                             x[j][2 + e] = m1 ? -INFINITY : fmaf(sc[j][2 + e], f, -mn);
                             const float by = al * ratio;
@@ -480,113 +522,116 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) acc[dt][j][k] *= ratio;
                 }
-                // weights, rounded to f16 for the product and the denominator alike (lt: as they
-                // are), packed per position and transposed into the V product's B fragments
+                // weights: summed in fp32, rounded to f16 for the product, packed per position and
+                // transposed into its B fragments
                 uint32_t bp[NT][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    uint16_t wl[2], wh[2];
-                    float ts[2];
+                    uint32_t hw[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float w0 = ex2(x[j][e]), w1 = ex2(x[j][2 + e]);
-                        uint32_t hw = pack_f16x2(w0, w1);
-                        const float2 wf = f16x2_to_f32x2(hw);
-                        ts[e] = w0 + w1;
-                        l[j][e] += wf.x + wf.y;
-                        lt[j][e] += ts[e];
-                        if (wmul != 1.f) hw = pack_f16x2(w0 * wmul, w1 * wmul);
-                        wl[e] = (uint16_t)(hw & 0xFFFFu);
-                        wh[e] = (uint16_t)(hw >> 16);
+                        float w0 = ex2(x[j][e]), w1 = ex2(x[j][2 + e]);
+                        x[j][e] = w0 + w1;
+                        l[j][e] += x[j][e];
+                        if (wmul != 1.f) w0 *= wmul, w1 *= wmul;
+                        hw[e] = pack_f16x2(w0, w1);
                     }
-                    bp[j][0] = transpose8((uint32_t)wl[0] | ((uint32_t)wl[1] << 16));
-                    bp[j][1] = transpose8((uint32_t)wh[0] | ((uint32_t)wh[1] << 16));
-                    if (!SPARSE && p.a.out_mass) {
+                    bp[j][0] = transpose8(__byte_perm(hw[0], hw[1], 0x5410));
+                    bp[j][1] = transpose8(__byte_perm(hw[0], hw[1], 0x7632));
+                }
+                if (!SPARSE && p.a.out_mass) {
+                    // the tile's sum of weights per row: 2 NT values summed over the 8 lanes of a
+                    // column, halving what a lane carries at each step; value v ends in lanes gid
+                    // with gid % (2 NT) = v
+                    float v[2 * NT], m[2 * NT];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float s = ts[e];
+                    for (int k = 0; k < 2 * NT; ++k) v[k] = x[k >> 1][k & 1], m[k] = mr[k >> 1][k & 1];
 #pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                            const int r = 8 * j + 2 * tig + e;
-                            if (gid == 0 && r < nrows) {
-                                const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
-                                p.tile_lse[(((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i) * p.tiles + tile] =
-                                    s > 0.f ? mr[j][e] + log2f(s) : s != s ? s : -INFINITY;
+                    for (int w = NT, o = 4 * NT; w; w >>= 1, o >>= 1) {
+                        const bool hi = lane & o;
+#pragma unroll
+                        for (int k = 0; k < w; ++k) {
+                            const float give = hi ? v[k] : v[k + w];
+                            v[k] = (hi ? v[k + w] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+                            m[k] = hi ? m[k + w] : m[k];
+                        }
+                    }
+#pragma unroll
+                    for (int o = 8 * NT; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                    const int k = gid & (2 * NT - 1), r = 8 * (k >> 1) + 2 * tig + (k & 1);
+                    if (gid < 2 * NT && r < nrows)
+                        mass_at[(int64_t)tile * mass_pitch + r] = v[0] > 0.f ? m[0] + log2f(v[0]) : v[0] != v[0] ? v[0] : -INFINITY;
+                }
+                // V^T (A) . W^T (B) over 16 positions: a lane holds kCols columns from col_of(gid)
+                // on of four positions; tile dt has column 2 dt of them in row gid, 2 dt + 1 in row
+                // gid + 8
+                const int vpos[4] = {pos_of<HD>(2 * tig), pos_of<HD>(2 * tig + 1), pos_of<HD>(2 * tig) + 8, pos_of<HD>(2 * tig + 1) + 8};
+#pragma unroll
+                for (int h = 0; h < (HD + 127) / 128; ++h) {
+                    uint32_t y[4][kWords];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t va = stage + S::kTile + h * 2048 + (k & 1 ? voff1 : voff0) + (k >> 1) * 8 * kPitch;
+                        if constexpr (HD == 64) {
+                            const uint2 v = lds2(va);
+                            y[k][0] = v.x, y[k][1] = v.y;
+                        } else {
+                            const uint4 v = lds4(va);
+                            y[k][0] = v.x, y[k][1] = v.y, y[k][2] = v.z, y[k][3] = v.w;
+                        }
+                    }
+                    // In a masked tile rows past the end are zeroed (0 * NaN is NaN), and NaN codes
+                    // of positions that only some rows see are taken out and given back to those
+                    int nan_at[kWords][4];
+                    bool nan_any = false;
+                    if (masked) {
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) nan_at[w][d] = 0x7fffffff;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int w = 0; w < kWords; ++w) {
+                                if (pos0 + vpos[k] >= vlim) y[k][w] = 0;
+                                const uint32_t isn = __vcmpeq4(y[k][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                nan_any = nan_any || isn;
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    if ((isn >> (8 * d)) & 1u) nan_at[w][d] = min(nan_at[w][d], pos0 + vpos[k]);
+                                y[k][w] &= ~isn;
                             }
-                        }
+                        nan_any = __any_sync(0xffffffffu, nan_any);
                     }
-                }
-                // V^T (A) . W^T (B) over 16 positions. Tile 2 mp + u2 has dim 32 mp + 4 gid + 2 u2
-                // in row gid and the next in row gid + 8, so that a thread's dims are one word per
-                // position. In a masked tile, rows past the end are zeroed (0 * NaN is NaN) and
-                // NaN codes taken out, to be given back to the rows that see them.
-                const int pr = 2 * tig;
-                bool nan_any = false;
-                if (masked) {
 #pragma unroll
-                    for (int mp = 0; mp < HD / 32; ++mp) {
-                        const int vc = 2 * mp + (gid >> 2), vo = 4 * (gid & 3);
+                    for (int w = 0; w < kWords; ++w)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int r = pr + (k & 1) + 8 * (k >> 1);
-                            uint32_t* y = const_cast<uint32_t*>(reinterpret_cast<const uint32_t*>(vs + chunk_at<HD>(r, vc) + vo));
-                            if (pos0 + r >= vlim) *y = 0;  // (each word of V belongs to one lane)
-                            else nan_any = nan_any || __vcmpeq4(*y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        for (int u2 = 0; u2 < 2; ++u2) {
+                            const uint32_t lo = __byte_perm(y[0][w], y[1][w], u2 ? 0x7362 : 0x5140);
+                            const uint32_t hi = __byte_perm(y[2][w], y[3][w], u2 ? 0x7362 : 0x5140);
+                            const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)(lo & 0xFFFFu)), a1 = e4m3x2_to_f16x2((uint16_t)(lo >> 16));
+                            const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)(hi & 0xFFFFu)), a3 = e4m3x2_to_f16x2((uint16_t)(hi >> 16));
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) mma_f16_16816(acc[8 * h + 2 * w + u2][j], a0, a1, a2, a3, bp[j][0], bp[j][1]);
                         }
-                    }
-                    nan_any = __any_sync(0xffffffffu, nan_any);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the copies that follow
-                }
-#pragma unroll
-                for (int mp = 0; mp < HD / 32; ++mp) {
-                    const int vc = 2 * mp + (gid >> 2), vo = 4 * (gid & 3);
-                    uint32_t y[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        y[k] = *reinterpret_cast<const uint32_t*>(vs + chunk_at<HD>(pr + (k & 1) + 8 * (k >> 1), vc) + vo);
-                    int nan_at[4];  // first position with a NaN, for each of the four dims
                     if (nan_any) {
 #pragma unroll
-                        for (int d = 0; d < 4; ++d) nan_at[d] = 0x7fffffff;
+                        for (int w = 0; w < kWords; ++w)
 #pragma unroll
-                        for (int k = 3; k >= 0; --k) {
-                            const uint32_t isn = __vcmpeq4(y[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            for (int d = 0; d < 4; ++d) {
+                                int at4 = nan_at[w][d];
+                                at4 = min(at4, __shfl_xor_sync(0xffffffffu, at4, 1));
+                                at4 = min(at4, __shfl_xor_sync(0xffffffffu, at4, 2));
 #pragma unroll
-                            for (int d = 0; d < 4; ++d)
-                                if ((isn >> (8 * d)) & 1u) nan_at[d] = min(nan_at[d], pos0 + pr + (k & 1) + 8 * (k >> 1));
-                            y[k] &= ~isn;
-                        }
+                                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            nan_at[d] = min(nan_at[d], __shfl_xor_sync(0xffffffffu, nan_at[d], 1));
-                            nan_at[d] = min(nan_at[d], __shfl_xor_sync(0xffffffffu, nan_at[d], 2));
-                        }
-                    }
-#pragma unroll
-                    for (int u2 = 0; u2 < 2; ++u2) {
-                        const uint32_t s0 = 0x0040u + 0x0022u * u2, s1 = s0 + 0x0011u;
-                        const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[0], y[1], s0));
-                        const uint32_t a1 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[0], y[1], s1));
-                        const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[2], y[3], s0));
-                        const uint32_t a3 = e4m3x2_to_f16x2((uint16_t)__byte_perm(y[2], y[3], s1));
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            mma_f16_16816(acc[2 * mp + u2][j], a0, a1, a2, a3, bp[j][0], bp[j][1]);
-                            if (nan_any)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int lim = lims[8 * j + 2 * tig + e];
-                                    if (nan_at[2 * u2] < lim) acc[2 * mp + u2][j][e] = __uint_as_float(0x7fc00000u);
-                                    if (nan_at[2 * u2 + 1] < lim) acc[2 * mp + u2][j][2 + e] = __uint_as_float(0x7fc00000u);
-                                }
-                        }
+                                    for (int e = 0; e < 2; ++e)
+                                        if (at4 < lims[8 * j + 2 * tig + e]) acc[8 * h + 2 * w + d / 2][j][2 * (d & 1) + e] = __uint_as_float(0x7fc00000u);
+                            }
                     }
                 }
             } else if (!SPARSE && p.a.out_mass) {
-                for (int r = lane; r < nrows; r += 32) {
-                    const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
-                    p.tile_lse[(((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i) * p.tiles + tile] = -INFINITY;
-                }
+                for (int r = lane; r < nrows; r += 32) mass_at[(int64_t)tile * mass_pitch + r] = -INFINITY;
             }
             __syncwarp();  // everyone is done with the stage
             issue();
@@ -602,10 +647,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], o);
-                    lt[j][e] += __shfl_xor_sync(0xffffffffu, lt[j][e], o);
-                }
+                for (int o = 4; o < 32; o <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], o);
         if (gid == 0)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -614,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     const int r = warp * R + 8 * j + 2 * tig + e;
                     redm[r] = mr[j][e];
                     redl[r] = l[j][e];
-                    redt[r] = lt[j][e];
                 }
         __syncthreads();
 #pragma unroll
@@ -626,16 +667,14 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) M = fmaxf(M, redm[w * R + r]);
                 const float mine = mr[j][e] == -INFINITY ? 0.f : ex2(mr[j][e] - M);
-                float L = 0.f, Lt = 0.f;
+                float L = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float f = redm[w * R + r] == -INFINITY ? 0.f : ex2(redm[w * R + r] - M);
                     L += f * redl[w * R + r];
-                    Lt += f * redt[w * R + r];
                 }
                 mr[j][e] = M;
                 l[j][e] = L;
-                lt[j][e] = Lt;
                 const float by = mine * vcur;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) {
@@ -683,23 +722,29 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     const bool some = !(l[j][e] <= 0.f);
                     const float inv = some ? 1.f / l[j][e] : 0.f;
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) {
-                        const int d = 32 * (dt / 2) + 4 * gid + 2 * (dt % 2);
-                        if (whole)
-                            *reinterpret_cast<uint32_t*>(p.a.out + row * HD + d) =
-                                some ? f32x2_to_bf16x2(acc[dt][j][e] * inv, acc[dt][j][2 + e] * inv) : 0u;
-                        else
-                            *reinterpret_cast<float2*>(slot + R * 4 + r * HD + d) = make_float2(acc[dt][j][e], acc[dt][j][2 + e]);
+                    for (int dt = 0; dt < DT; dt += 4) {  // 8 columns
+                        const int d = (dt >> 3) * 128 + col_of<HD>(gid) + 2 * (dt & 7);
+                        if (whole) {
+                            uint32_t o4[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                o4[k] = some ? f32x2_to_bf16x2(acc[dt + k][j][e] * inv, acc[dt + k][j][2 + e] * inv) : 0u;
+                            *reinterpret_cast<uint4*>(p.a.out + row * HD + d) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2)
+                                *reinterpret_cast<float4*>(slot + R * 4 + r * HD + d + 2 * k) =
+                                    make_float4(acc[dt + k][j][e], acc[dt + k][j][2 + e], acc[dt + k + 1][j][e], acc[dt + k + 1][j][2 + e]);
+                        }
                     }
                     if (gid == 0) {
                         if (whole) {
-                            const float lse2 = some ? mr[j][e] + log2f(lt[j][e]) : -INFINITY;
+                            const float lse2 = some ? mr[j][e] + log2f(l[j][e]) : -INFINITY;
                             if (p.a.out_lse) p.a.out_lse[row] = lse2 * kLn2;
-                            if (!SPARSE && p.a.out_mass) p.row_lse[row] = lse2;
+                            if (!SPARSE && p.a.out_mass) p.row_lse[((int64_t)b * p.c.nkv + g) * mass_pitch + row0 + r] = lse2;
                         } else {
                             slot[r] = mr[j][e];
                             slot[R + r] = l[j][e];
-                            slot[2 * R + r] = lt[j][e];
                         }
                     }
                 }
@@ -729,34 +774,32 @@ __global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_const
     const int g = head / p.group;
     const int r_abs = SPARSE ? head - g * p.group : tok * p.group + head - g * p.group;
     const int part = SPARSE ? tok : r_abs / R, r = SPARSE ? r_abs : r_abs - part * R;
-    float M = -INFINITY, L = 0.f, Lt = 0.f, a[V];
+    float M = -INFINITY, L = 0.f, a[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a[v] = 0.f;
     if (sw.tiles > 0) {
-        const int64_t per = *p.per, base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
-        const int64_t c0 = base / per, c1 = (base + sw.tiles - 1) / per;
+        const int per = *p.per, base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
+        const int c0 = base / per, c1 = (base + sw.tiles - 1) / per;
         if (c0 == c1) return;  // finished by one CTA
         const float* parts = p.parts;
         // in CTA c0 the unit is the last (slot 1) unless it is also the first; in later ones the first
-        auto slot = [&](int64_t c) {
-            return parts + (c * 2 + (c == c0 && base != c0 * per ? 1 : 0)) * (int64_t)(R * (HD + 4));
+        auto slot = [&](int c) {
+            return parts + (int64_t)(c * 2 + (c == c0 && base != c0 * per ? 1 : 0)) * (R * (HD + 4));
         };
-        for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[r]);
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[r]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int64_t c = c0 + lane; c <= c1; c += 32) {
+        for (int c = c0 + lane; c <= c1; c += 32) {
             const float* s = slot(c);
             const float f = s[r] == -INFINITY ? 0.f : ex2(s[r] - M);
             L += f * s[R + r];
-            Lt += f * s[2 * R + r];
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             L += __shfl_xor_sync(0xffffffffu, L, o);
-            Lt += __shfl_xor_sync(0xffffffffu, Lt, o);
         }
 #pragma unroll 4
-        for (int64_t c = c0 + wr; c <= c1; c += WPR) {
+        for (int c = c0 + wr; c <= c1; c += WPR) {
             const float* s = slot(c);
             const float f = s[r] == -INFINITY ? 0.f : ex2(s[r] - M);
             const float* x = s + R * 4 + r * HD + lane * V;
@@ -782,31 +825,43 @@ __global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_const
     for (int v = 0; v < V; v += 2)
         *reinterpret_cast<uint32_t*>(out + v) = some ? f32x2_to_bf16x2(a[v] * inv, a[v + 1] * inv) : 0u;
     if (lane == 0) {
-        const float lse2 = some ? M + log2f(Lt) : -INFINITY;
+        const float lse2 = some ? M + log2f(L) : -INFINITY;
         if (p.a.out_lse) p.a.out_lse[row] = lse2 * kLn2;
-        if (!SPARSE && p.a.out_mass) p.row_lse[row] = lse2;
+        if (!SPARSE && p.a.out_mass) p.row_lse[((int64_t)b * p.c.nkv + g) * p.t.T * p.group + r_abs] = lse2;
     }
 }
 
-// out_mass[b, j]: one thread per logical block, the tokens and heads summed in order.
-__global__ void __launch_bounds__(128) block_mass_kernel(const __grid_constant__ AttnParams p) {
-    const int b = blockIdx.y;
-    const int64_t j = (int64_t)blockIdx.x * 128 + threadIdx.x;
+// out_mass[b, j] over a CTA's 32 tiles: a thread sums one tile's rows of every eighth kv head in
+// order, then the eight sums and the block's tiles are added in order.
+__global__ void __launch_bounds__(256) block_mass_kernel(const __grid_constant__ AttnParams p) {
+    __shared__ float sums[8][32];
+    const int b = blockIdx.y, t = threadIdx.x & 31, gs = threadIdx.x >> 5;
+    const int tile = (int)blockIdx.x * 32 + t;
     pdl_wait();
-    if (j >= p.t.n_table) return;
-    const SeqStep s = seq_step(p.t, b);
-    const int tpb = p.c.bs / 16;
-    const int64_t at = (int64_t)b * p.t.n_table + j;
-    const int ntiles = (int)min((int64_t)tpb, (s.len + 15) / 16 - j * tpb);
+    const SeqWork w = seq_work<1, false>(p, b);
+    const int pitch = (int)p.t.T * p.group, rows = w.q * p.group;
     float sum = 0.f;
-    if (ntiles > 0)
-        for (int64_t row = (int64_t)b * p.t.T * p.a.nq, end = row + (int64_t)s.q * p.a.nq; row < end; ++row) {
-            const float L = p.row_lse[row];
-            for (int u = 0; u < ntiles; ++u) {
-                const float x = p.tile_lse[row * p.tiles + j * tpb + u];
-                if (x != -INFINITY) sum += exp2f(x - L);
+    if (tile < w.tiles)
+        for (int g = gs; g < p.c.nkv; g += 8) {
+            const int64_t head = (int64_t)b * p.c.nkv + g;
+            const float* x = p.tile_lse + (head * p.tiles + tile) * pitch;
+            const float* L = p.row_lse + head * pitch;
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+                const float v = x[r];
+                sum += v == -INFINITY ? 0.f : ex2(v - L[r]);
             }
         }
+    sums[gs][t] = sum;
+    __syncthreads();
+    const int per = 1 << p.tile_shift;  // tiles per block
+    const int64_t j = ((int64_t)blockIdx.x * 32 >> p.tile_shift) + threadIdx.x;
+    if (threadIdx.x >= 32 >> p.tile_shift || j >= p.t.n_table) return;
+    sum = 0.f;
+    for (int u = 0; u < per; ++u)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += sums[k][threadIdx.x * per + u];
+    const int64_t at = (int64_t)b * p.t.n_table + j;
     p.a.out_mass[at] = (p.a.mass ? p.a.mass[at] : 0.f) + sum;
 }
 
@@ -829,7 +884,7 @@ Layout layout_of(const BlockCache& c, int B, int64_t T, int nq, int64_t n_table,
     l.units = (int64_t)B * c.nkv * (sparse ? T : l.row_tiles);
     l.tiles = n_table * (c.bs / 16);
     l.base = 16;
-    l.parts = l.base + up16((size_t)l.units * 8);
+    l.parts = l.base + up16((size_t)l.units * 4);
     l.row_lse = l.parts + (size_t)2 * kMaxGrid * 8 * l.nt * (c.hd + 4) * 4;
     const size_t q_rows = (size_t)B * T * nq;
     l.tile_lse = l.row_lse + (mass ? up16(q_rows * 4) : 0);
@@ -928,8 +983,10 @@ cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const Bl
     const Layout l = layout_of(c, t.B, t.T, a.nq, t.n_table, sparse, a.out_mass != nullptr);
     if ((int64_t)t.B * t.T * a.nq > INT32_MAX) return cudaErrorInvalidValue;
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    AttnParams p{c, t, a, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int64_t*>(ws),
-                 reinterpret_cast<int64_t*>(ws + l.base), reinterpret_cast<float*>(ws + l.parts),
+    // tiles of all units on one line: 32-bit indices
+    if ((double)l.units * (double)(sparse ? (int64_t)a.n_sel * (c.bs / 16) : l.tiles) >= 2147483648.0) return cudaErrorInvalidValue;
+    AttnParams p{c, t, a, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int32_t*>(ws),
+                 reinterpret_cast<int32_t*>(ws + l.base), c.bs == 16 ? 0 : c.bs == 32 ? 1 : 2, reinterpret_cast<float*>(ws + l.parts),
                  reinterpret_cast<float*>(ws + l.row_lse), reinterpret_cast<float*>(ws + l.tile_lse)};
     int dev = 0, sms = 148;
     cudaError_t e;
@@ -940,7 +997,7 @@ cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const Bl
     e = c.hd == 64 ? launch_attn_hd<64>(l.nt, p, km, vm, sms, s)
                    : c.hd == 128 ? launch_attn_hd<128>(l.nt, p, km, vm, sms, s) : launch_attn_hd<256>(l.nt, p, km, vm, sms, s);
     if (e != cudaSuccess || !a.out_mass) return e;
-    return launch_after(block_mass_kernel, dim3((unsigned)((t.n_table + 127) / 128), (unsigned)t.B), 128, 0, s, p);
+    return launch_after(block_mass_kernel, dim3((unsigned)((l.tiles + 31) / 32), (unsigned)t.B), 256, 0, s, p);
 }
 
 }  // namespace mtp
