@@ -17,9 +17,10 @@
 // bits every time).
 //
 // Bound by HBM: every code is read once per row tile. Each of a CTA's four warps owns a ring of
-// tile stages (K and V, 16 rows each): it takes every fourth tile of the stretch, looks up its
-// blocks ahead and issues their tensor copies into the stage it has just used, across units,
-// so the warps meet only at a unit's end. Both contractions run on mma.sync m16n8k16 in f16 with fp32 sums: a tile has at most 32
+// stages: it takes every fourth step (one or two tiles of K and V) of the stretch and issues
+// their tensor copies into the stage it has just used, across units, so the warps meet only at
+// a unit's end. The blocks and scales of up to 32 tiles ahead are looked up by the warp's lanes
+// at once. The two tiles of a step keep two chains of dependent products going. Both contractions run on mma.sync m16n8k16 in f16 with fp32 sums: a tile has at most 32
 // query rows, far from where tcgen05's 128-row tiles would pay, and E4M3 decodes to f16
 // exactly (q is scaled per row by a power of two).
 #include <cuda.h>
@@ -51,30 +52,37 @@ struct AttnParams {
     int group;
     int row_tiles;       // dense: row tiles of 8 NT rows that T tokens have at most
     int64_t tiles;       // 16-position tiles of n_table blocks (tile_lse's pitch)
-    int32_t* per;        // [1] tiles per CTA
-    int32_t* unit_base;  // [units] first tile of each unit on the line
+    int32_t* per;        // [1] steps per CTA
+    int32_t* unit_base;  // [units] first step of each unit on the line
     int tile_shift;      // log2(16-position tiles per block)
+    uint32_t group_inv;  // ceil(2^20 / group): r / group = r group_inv >> 20 for r <= 1024
     float* parts;        // [2 kMaxGrid][8 NT (hd + 4)] partial sums of a CTA's first and last unit
     float* row_lse;      // [B, nkv, T group] base-2 log-sum-exp (with mass)
     float* tile_lse;     // [B, nkv, tiles, T group] of each tile's positions (with mass)
 };
 
-// A sequence's units and the tiles each has.
+// A sequence's units, outer * inner of them (dense: kv heads, each with its row tiles, the later
+// ones of which find their codes in L2; listed blocks: tokens, each with its kv heads), and the
+// tiles and steps of `P` tiles that each has.
 struct SeqWork {
-    int len, q, units, tiles;
+    int len, q, outer, inner, tiles, steps;
 };
-template <int NT, bool SPARSE>
+template <int NT, bool SPARSE, int P>
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
     const SeqStep s = seq_step(p.t, b);
-    SeqWork w{s.len, s.q, 0, 0};
+    SeqWork w;
+    w.len = s.len;
+    w.q = s.q;
     if (SPARSE) {
-        w.units = s.q * p.c.nkv;
+        w.outer = s.q;
+        w.inner = p.c.nkv;
         w.tiles = s.len > 0 ? p.a.n_sel << p.tile_shift : 0;
     } else {
-        w.units = p.c.nkv * ((s.q * p.group + 8 * NT - 1) / (8 * NT));
-        const int nb = blocks_of(s.len, p.c.bs, p.t.n_table);
-        w.tiles = min((s.len >> 4) + ((s.len & 15) != 0), nb << p.tile_shift);
+        w.outer = p.c.nkv;
+        w.inner = (s.q * p.group + 8 * NT - 1) / (8 * NT);
+        w.tiles = (int)min((int64_t)(s.len >> 4) + ((s.len & 15) != 0), p.tiles);
     }
+    w.steps = (w.tiles + P - 1) / P;
     return w;
 }
 
@@ -86,23 +94,27 @@ __device__ __forceinline__ int64_t unit_index(const AttnParams& p, int b, int g,
 
 template <int HD, int NT>
 struct Shape {
-    static constexpr int kTile = 16 * HD;                       // bytes of K (or V) in a stage
+    static constexpr int kTile = 16 * HD;                        // bytes of K (or V) of a tile
+    static constexpr int P = HD == 256 ? 1 : 2;                  // tiles per step
+    static constexpr int kJoint = HD == 256 || NT == 4 ? 1 : P;  // of them worked on together (registers)
     static constexpr int kPerSm = HD == 256 || NT >= 2 ? 2 : 3;  // CTAs per SM
-    static constexpr int kQPitch = HD + 8;                      // f16 elements
+    static constexpr int kQPitch = HD + 8;                       // f16 elements
     static constexpr int kRows = 8 * NT;
-    static constexpr size_t kFixed = (size_t)HD * NT * 64         // two warps' accumulators
+    static constexpr size_t kFixed = (size_t)HD * NT * 64           // two warps' accumulators
                                      + (size_t)kRows * kQPitch * 2  // q
                                      + (size_t)kRows * 8            // score factors, limits
                                      + (size_t)2 * kWarps * kRows * 4 + 16;
-    static constexpr size_t kStage = (size_t)kWarps * (2 * kTile + 16 + 8);  // tiles, info, barriers
+    static constexpr size_t kStage = (size_t)kWarps * (P * (2 * kTile + 16) + 8);  // tiles, info, barrier
     // (1 KB of each CTA's share of the SM's 228 KB is the system's)
     static constexpr int kStages = (int)(((size_t)(228 * 1024) / kPerSm - 1024 - kFixed) / kStage);
     static constexpr size_t kSmem = kStages * kStage + kFixed;
     static_assert(kStages >= 2, "two stages at least");
 };
 
+constexpr int kNowhere = 1 << 30;  // a position behind every limit (limits are clamped to it)
+
 struct TileInfo {
-    int pos0;  // first position, or -1: nothing to read
+    int pos0;  // first position, or kNowhere: nothing was read
     float ks, vs;
     int pad;
 };
@@ -122,13 +134,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-__device__ __forceinline__ void copy4_async(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-// Arrive on `bar` (one of its expected arrivals) when this thread's earlier cp.async are done.
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, int x, int row, int head, int block,
                                           uint64_t* bar) {
@@ -158,7 +163,7 @@ __device__ __forceinline__ uint32_t swizzled(int row, int byte) {  // row < 16, 
 }
 // Offset of what lane column group gid reads of MMA row m of V (its first half of 256 columns).
 template <int HD>
-__device__ __forceinline__ uint32_t S_voff(int m, int gid) {
+__device__ __forceinline__ uint32_t v_offset(int m, int gid) {
     return HD == 64 ? swizzled<HD>(pos_of<HD>(m), col_of<HD>(gid) & ~15) + (col_of<HD>(gid) & 15)
                     : swizzled<HD>(pos_of<HD>(m), col_of<HD>(gid));
 }
@@ -183,40 +188,41 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     block_attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
     using S = Shape<HD, NT>;
-    constexpr int ST = S::kStages, KC = HD / 16, DT = HD / 16, R = S::kRows, QP = S::kQPitch;
-    extern __shared__ __align__(1024) uint8_t raw[];
-    uint8_t* ring = raw;  // [warp][stage][K, V][16 rows]
-    float4* xacc = reinterpret_cast<float4*>(ring + (size_t)kWarps * ST * 2 * S::kTile);  // [2][DT NT][32]
-    TileInfo* info = reinterpret_cast<TileInfo*>(xacc + 2 * DT * NT * 32);               // [warp][stage]
-    uint64_t* full = reinterpret_cast<uint64_t*>(info + kWarps * ST);                    // [warp][stage]
-    uint16_t* qh = reinterpret_cast<uint16_t*>(full + kWarps * ST);                      // [R][QP] f16
-    float* hfac = reinterpret_cast<float*>(qh + R * QP);                                 // [R]
-    int* lims = reinterpret_cast<int*>(hfac + R);                                        // [R]
-    float* redm = reinterpret_cast<float*>(lims + R);                                    // [warp][R]
+    constexpr int ST = S::kStages, P = S::P, HJ = S::kJoint, KC = HD / 16, DT = HD / 16, R = S::kRows, QP = S::kQPitch;
+    constexpr uint32_t kStageBytes = P * 2 * S::kTile;                                    // of one warp
+    extern __shared__ __align__(1024) uint8_t ring[];                                     // [warp][stage][tile][K, V][16 rows]
+    float4* xacc = reinterpret_cast<float4*>(ring + (size_t)kWarps * ST * kStageBytes);   // [2][DT NT][32]
+    TileInfo* info = reinterpret_cast<TileInfo*>(xacc + 2 * DT * NT * 32);                // [warp][stage][tile]
+    uint64_t* full = reinterpret_cast<uint64_t*>(info + kWarps * ST * P);                 // [warp][stage]
+    uint16_t* qh = reinterpret_cast<uint16_t*>(full + kWarps * ST);                       // [R][QP] f16
+    float* hfac = reinterpret_cast<float*>(qh + R * QP);                                  // [R]
+    int* lims = reinterpret_cast<int*>(hfac + R);                                         // [R]
+    float* redm = reinterpret_cast<float*>(lims + R);                                     // [warp][R]
     float* redl = redm + kWarps * R;
     volatile int* abort = reinterpret_cast<volatile int*>(redl + kWarps * R);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
-    if (smem_u32(raw) & 1023u) {  // (the swizzled copies need it; dynamic shared memory starts there)
+    const uint32_t ring_at = smem_u32(ring);
+    if (ring_at & 1023u) {  // (the swizzled copies need it; dynamic shared memory starts there)
         if (tid == 0) raise_flag(p.t.dev_err, DEVFLAG_TIMEOUT);
         return;
     }
-    if (tid < kWarps * ST) mbar_init(&full[tid], 2);  // lane 0's arrival and its scale copies'
+    if (tid < kWarps * ST) mbar_init(&full[tid], 1);
     if (tid == 0) *abort = 0;
     mbar_fence_init();
     __syncthreads();
     pdl_wait();  // everything below reads or writes memory that earlier kernels may still use
 
-    // this CTA's stretch of the line: [beg, end), its first sequence, unit and tile (every warp
-    // for itself: two passes over the lengths, 32 sequences at a time)
+    // this CTA's stretch of the line: `stretch` steps from `beg` on, and the sequence, unit and
+    // step it starts with (every warp for itself, 32 sequences at a time)
     const int B = p.t.B;
-    int total = 0;
-    for (int b0 = 0; b0 < B; b0 += 32)
-        if (b0 + lane < B) {
-            const SeqWork w = seq_work<NT, SPARSE>(p, b0 + lane);
-            total += w.units * w.tiles;
-        }
+    SeqWork w0 = seq_work<NT, SPARSE, P>(p, min(lane, B - 1));
+    int n0 = lane < B ? w0.outer * w0.inner * w0.steps : 0, total = n0;
+    for (int b = 32 + lane; b < B; b += 32) {
+        const SeqWork w = seq_work<NT, SPARSE, P>(p, b);
+        total += w.outer * w.inner * w.steps;
+    }
     total = __reduce_add_sync(0xffffffffu, total);
     const int grid = (int)gridDim.x;
     const int per = (total / grid + (total % grid != 0) + kWarps - 1) / kWarps * kWarps;
@@ -224,119 +230,134 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     if ((int64_t)blockIdx.x * per >= total) return;
     const int beg = (int)blockIdx.x * per;
     const int stretch = min(total - beg, per);
-    int b = 0, u = 0, t0 = 0;
-    {
-        int before = 0;
-        for (int b0 = 0; b0 < B; b0 += 32) {
-            SeqWork w{0, 0, 0, 0};
-            if (b0 + lane < B) w = seq_work<NT, SPARSE>(p, b0 + lane);
-            const int n = w.units * w.tiles;
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            const uint32_t past = __ballot_sync(0xffffffffu, before + inc > beg);
-            if (past) {
-                const int src = __ffs(past) - 1;
-                const int off = beg - (before + __shfl_sync(0xffffffffu, inc - n, src));
-                const int tiles = __shfl_sync(0xffffffffu, w.tiles, src);
-                b = b0 + src;
-                u = off / tiles;
-                t0 = off - u * tiles;
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, inc, 31);
-        }
-    }
-    // A place on the line: a unit (kv head g; row tile or token `part`) and the tiles [t0, t1) of
-    // it that belong to this CTA.
+
+    // A place on the line: a unit and the steps [t0, t1) of it that belong to this CTA.
     struct Place {
         SeqWork sw;
-        int b, u, g, part, t0, t1;
-        int left;  // tiles of the stretch from t0 on
+        int b, outer, inner, t0, t1;
+        int left;  // steps of the stretch from t0 on
     };
-    auto settle = [&](Place& c) {
-        if (SPARSE) {
-            c.part = c.u / p.c.nkv;
-            c.g = c.u - c.part * p.c.nkv;
-        } else {  // a head's row tiles in turn: the later ones find its tiles in L2
-            const int rt = c.sw.units / p.c.nkv;
-            c.g = c.u / rt;
-            c.part = c.u - c.g * rt;
+    Place pl;
+    for (int b0 = 0, before = 0;; b0 += 32) {
+        if (b0) {
+            w0 = seq_work<NT, SPARSE, P>(p, min(b0 + lane, B - 1));
+            n0 = b0 + lane < B ? w0.outer * w0.inner * w0.steps : 0;
         }
-        c.t1 = min(c.sw.tiles, c.t0 + c.left);
-    };
+        int inc = n0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + inc > beg);
+        if (past) {  // (some chunk has it: beg < total)
+            const int src = __ffs(past) - 1;
+            const int off = beg - (before + __shfl_sync(0xffffffffu, inc - n0, src));
+            pl.sw.len = __shfl_sync(0xffffffffu, w0.len, src);
+            pl.sw.q = __shfl_sync(0xffffffffu, w0.q, src);
+            pl.sw.outer = __shfl_sync(0xffffffffu, w0.outer, src);
+            pl.sw.inner = __shfl_sync(0xffffffffu, w0.inner, src);
+            pl.sw.tiles = __shfl_sync(0xffffffffu, w0.tiles, src);
+            pl.sw.steps = __shfl_sync(0xffffffffu, w0.steps, src);
+            pl.b = b0 + src;
+            const int u = off / pl.sw.steps;
+            pl.t0 = off - u * pl.sw.steps;
+            pl.outer = u / pl.sw.inner;
+            pl.inner = u - pl.outer * pl.sw.inner;
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    pl.left = stretch;
+    pl.t1 = min(pl.sw.steps, pl.t0 + pl.left);
     auto next_unit = [&](Place& c) -> bool {  // false at the stretch's end
         c.left -= c.t1 - c.t0;
         if (c.left <= 0) return false;
         c.t0 = 0;
-        if (++c.u == c.sw.units) {
-            c.u = 0;
-            do c.sw = seq_work<NT, SPARSE>(p, ++c.b);
-            while (c.sw.units * c.sw.tiles == 0 && c.b + 1 < B);
+        if (++c.inner == c.sw.inner) {
+            c.inner = 0;
+            if (++c.outer == c.sw.outer) {
+                c.outer = 0;
+                do c.sw = seq_work<NT, SPARSE, P>(p, ++c.b);
+                while (c.sw.outer * c.sw.inner * c.sw.steps == 0 && c.b + 1 < B);
+            }
         }
-        settle(c);
+        c.t1 = min(c.sw.steps, c.left);
         return true;
     };
-    Place pl;
-    pl.sw = seq_work<NT, SPARSE>(p, b);
-    pl.b = b;
-    pl.u = u;
-    pl.t0 = t0;
-    pl.left = stretch;
-    settle(pl);
 
-    // The copies' side of this warp, up to ST tiles ahead: its next tile, whose block is looked
-    // up one issue before it is needed.
+    // The copies' side of this warp, ST steps ahead. Lane l looks up tile l % P of the warp's
+    // step l / P from ah_step on; ah_n counts the steps of those that have been issued.
     Place ah = pl;
-    int ah_tile = ah.t0 + warp, ah_blk = -1, ah_lb = -1;
+    int ah_step = ah.t0 + warp, ah_n = 0, ah_cnt = 0, ah_blk = -1, ah_pos = kNowhere;
+    float ah_ks = 0.f, ah_vs = 0.f;
+    uint32_t ah_read = 0;
     bool ah_more = true;
     int ist = 0;  // the stage the next copies go to
-    auto look_up = [&]() {  // ah_tile may lie past its unit: on to the next ones
-        while (ah_tile >= ah.t1) {
+    auto look_up = [&]() {
+        while (ah_step >= ah.t1) {  // past its unit: on to the next ones
             if (!next_unit(ah)) {
                 ah_more = false;
                 return;
             }
-            ah_tile = ah.t0 + warp;
+            ah_step = ah.t0 + warp;
         }
-        const int e = ah_tile >> p.tile_shift;
-        ah_lb = SPARSE ? __ldg(p.a.sel + (((int64_t)ah.b * p.t.T + ah.part) * p.c.nkv + ah.g) * p.a.n_sel + e) : e;
-        ah_blk = ah_lb < 0 ? -1 : table_block(p.t, p.c.num_blocks, ah.b, ah_lb);
+        ah_n = 0;
+        ah_cnt = min(32 / P, (ah.t1 - ah_step + kWarps - 1) / kWarps);
+        const int tile = (ah_step + lane / P * kWarps) * P + lane % P;
+        const bool mine = lane / P < ah_cnt && tile < ah.sw.tiles;
+        const int g = SPARSE ? ah.inner : ah.outer;
+        int lb = tile >> p.tile_shift, lim = ah.sw.len;
+        if (SPARSE) {
+            lim += ah.outer + 1 - ah.sw.q;
+            lb = mine ? __ldg(p.a.sel + (((int64_t)ah.b * p.t.T + ah.outer) * p.c.nkv + g) * p.a.n_sel + lb) : -1;
+        }
+        const int64_t pos = ((int64_t)lb << (4 + p.tile_shift)) + 16 * (tile & ((1 << p.tile_shift) - 1));
+        const bool seen = mine && lb >= 0 && pos < lim;
+        ah_blk = seen ? table_block(p.t, p.c.num_blocks, ah.b, lb) : -1;
+        if (seen && ah_blk < 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
+        ah_pos = kNowhere;
+        ah_ks = ah_vs = 0.f;
+        if (ah_blk >= 0) {
+            const int64_t at = (int64_t)ah_blk * p.c.nkv + g;
+            ah_ks = p.c.k_scale[at];
+            ah_vs = p.c.v_scale[at];
+            ah_pos = (int)pos;
+        }
+        ah_read = __ballot_sync(0xffffffffu, ah_blk >= 0);
     };
     auto issue = [&]() {
         if (!ah_more) return;
+        if (*abort) {  // a wait ran out: no more copies
+            ah_more = false;
+            return;
+        }
         const int at = warp * ST + ist;
-        if (lane == 0) {
-            const int lim = SPARSE ? ah.sw.len - ah.sw.q + ah.part + 1 : ah.sw.len;
-            const int row = 16 * (ah_tile & ((1 << p.tile_shift) - 1));
-            const int64_t pos0 = (int64_t)ah_lb * p.c.bs + row;
-            const bool seen = ah_lb >= 0 && pos0 < lim;
-            if (seen && ah_blk < 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
-            const bool read = seen && ah_blk >= 0 && !*abort;
-            info[at].pos0 = read ? (int)pos0 : -1;
-            if (read) {
-                uint8_t* kd = ring + (size_t)at * 2 * S::kTile;
-                const int64_t sc = (int64_t)ah_blk * p.c.nkv + ah.g;
-                mbar_arrive_expect_tx(&full[at], 2 * S::kTile);
+        if (lane == 0) mbar_arrive_expect_tx(&full[at], (uint32_t)__popc((ah_read >> (ah_n * P)) & ((1u << P) - 1u)) * 2u * S::kTile);
+        __syncwarp();
+        if (lane / P == ah_n) {
+            TileInfo ti;
+            ti.pos0 = ah_pos;
+            ti.ks = ah_ks;
+            ti.vs = ah_vs;
+            ti.pad = 0;
+            info[at * P + lane % P] = ti;
+            if (ah_blk >= 0) {
+                uint8_t* kd = ring + (size_t)at * kStageBytes + (lane % P) * 2 * S::kTile;
+                const int row = ah_pos & ((16 << p.tile_shift) - 1);
+                const int g = SPARSE ? ah.inner : ah.outer;
 #pragma unroll
                 for (int x = 0; x < HD; x += 128) {
-                    load_tile(kd + x * 16, &kmap, x, row, ah.g, ah_blk, &full[at]);
-                    load_tile(kd + S::kTile + x * 16, &vmap, x, row, ah.g, ah_blk, &full[at]);
+                    load_tile(kd + x * 16, &kmap, x, row, g, ah_blk, &full[at]);
+                    load_tile(kd + S::kTile + x * 16, &vmap, x, row, g, ah_blk, &full[at]);
                 }
-                copy4_async(&info[at].ks, p.c.k_scale + sc);
-                copy4_async(&info[at].vs, p.c.v_scale + sc);
-                copies_arrive(&full[at]);
-            } else {
-                mbar_arrive(&full[at]);
-                mbar_arrive(&full[at]);
             }
         }
         if (++ist == ST) ist = 0;
-        ah_tile += kWarps;
-        look_up();
+        if (++ah_n == ah_cnt) {
+            ah_step += ah_cnt * kWarps;
+            look_up();
+        }
     };
     look_up();
 #pragma unroll 1
@@ -344,27 +365,28 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 
     const int gid = lane >> 2, tig = lane & 3;
     constexpr int kPitch = HD == 64 ? 64 : 128, kWords = HD == 64 ? 2 : 4;  // of a (half) tile; words a lane holds of a V row
-    const uint32_t ring_at = smem_u32(ring);
     const uint32_t koff = swizzled<HD>(pos_of<HD>(gid), 16 * tig);
-    const uint32_t voff0 = S_voff<HD>(2 * tig, gid), voff1 = S_voff<HD>(2 * tig + 1, gid);
+    const uint32_t voff0 = v_offset<HD>(2 * tig, gid), voff1 = v_offset<HD>(2 * tig + 1, gid);
     int st = 0;
     uint32_t ph = 0;
     bool first = true;  // this CTA's first unit
     do {
         const SeqWork& sw = pl.sw;
-        const int b = pl.b, g = pl.g, part = pl.part, t0 = pl.t0, t1 = pl.t1;
-        // rows of this unit: row r is token tok, head i of the group, r_abs = tok group + i
+        const int b = pl.b, g = SPARSE ? pl.inner : pl.outer, part = SPARSE ? pl.outer : pl.inner, t0 = pl.t0, t1 = pl.t1;
+        // rows of this unit: row r is token tok, head i of the group, row0 + r = tok group + i
         const int row0 = SPARSE ? part * p.group : part * R;
         const int nrows = SPARSE ? p.group : min(R, sw.q * p.group - row0);
-        const int tok0 = row0 / p.group;
-        const int lim0 = sw.len - sw.q + tok0 + 1;        // the fewest positions a row sees
-        const int vlim = SPARSE ? lim0 : sw.len;          // rows from here on hold nothing
-        const int mass_pitch = (int)p.t.T * p.group;  // rows of a kv head
+        auto token_of = [&](int r) { return (int)(((uint32_t)(row0 + r) * p.group_inv) >> 20); };
+        const int lim0 = min(sw.len - sw.q + token_of(0) + 1, kNowhere);  // the fewest positions a row sees
+        const int vlim = SPARSE ? lim0 : sw.len;                          // rows from here on hold nothing
+        const int mass_pitch = (int)p.t.T * p.group;                      // rows of a kv head
         float* mass_at = nullptr;
         if (!SPARSE && p.a.out_mass) mass_at = p.tile_lse + ((int64_t)b * p.c.nkv + g) * p.tiles * mass_pitch + row0;
-        if (!SPARSE && tid == 0 && t1 == sw.tiles && (sw.len - 1) / p.c.bs >= p.t.n_table)
-            raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);  // positions past the table
-        if (t0 == 0 && tid == 0) p.unit_base[unit_index<SPARSE>(p, b, g, part)] = beg + (stretch - pl.left);
+        if (tid == 0) {
+            if (!SPARSE && t1 == sw.steps && (sw.len - 1) / p.c.bs >= p.t.n_table)
+                raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);  // positions past the table
+            if (t0 == 0) p.unit_base[unit_index<SPARSE>(p, b, g, part)] = beg + (stretch - pl.left);
+        }
 
         __syncthreads();  // the previous unit's rows and sums are no longer needed
         {
@@ -372,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             constexpr int LH = HD / 8, HPL = 32 / LH;  // lanes per row, rows per warp at a time
             for (int r = warp * HPL + lane / LH; r < R; r += kWarps * HPL) {
                 const bool has = r < nrows;
-                const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
+                const int tok = token_of(r), i = (row0 + r) - tok * p.group;
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (has)
                     v = *reinterpret_cast<const uint4*>(p.a.q + ((int64_t)b * p.t.T + tok) * p.a.q_stride +
@@ -383,15 +405,18 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
 #pragma unroll
                 for (int o = LH / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                // e within [-113, 126], so that 2^e and 2^-e are normal (an all but zero row keeps
+                // a smaller largest value)
                 const bool fin = mx < INFINITY;
-                const int e = mx > 0.f && fin ? 14 - ilogbf(mx) : 0;
+                const int e = fin ? min(141 - (int)(__float_as_uint(mx) >> 23), 126) : 0;
+                const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
                 uint32_t o4[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o4[k] = pack_f16x2(ldexpf(bf16_lo(w[k]), e), ldexpf(bf16_hi(w[k]), e));
+                for (int k = 0; k < 4; ++k) o4[k] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
                 *reinterpret_cast<uint4*>(qh + r * QP + 8 * (lane % LH)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
                 if (lane % LH == 0) {
-                    hfac[r] = !has ? 0.f : fin ? ldexpf(p.a.scale * kLog2e, -e) : __uint_as_float(0x7fc00000u);
-                    lims[r] = has ? sw.len - sw.q + tok + 1 : 0x7fffffff;
+                    hfac[r] = !has ? 0.f : fin ? p.a.scale * kLog2e * down : __uint_as_float(0x7fc00000u);
+                    lims[r] = has ? min(sw.len - sw.q + tok + 1, kNowhere) : kNowhere;
                 }
             }
         }
@@ -419,219 +444,249 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 for (int k = 0; k < 4; ++k) acc[dt][j][k] = 0.f;
         }
 
-        for (int tile = t0 + warp; tile < t1; tile += kWarps) {
+#pragma unroll 1
+        for (int step = t0 + warp; step < t1; step += kWarps) {
             const int at = warp * ST + st;
             if (!mbar_try_wait(&full[at], ph)) wait_long(&full[at], ph, abort, p.t.dev_err);
-            const int pos0 = info[at].pos0;
-            if (pos0 >= 0) {
-                const uint32_t stage = ring_at + (uint32_t)at * (2 * S::kTile);
-                const float kscale = info[at].ks, vscale = info[at].vs;
+#pragma unroll
+            for (int h0 = 0; h0 < P; h0 += HJ) {
+                int pos0[HJ];
+                float ks[HJ], vs[HJ], sc[HJ][NT][4], x[HJ][NT][4];
+                bool masked = false;  // a limit per row matters
+#pragma unroll
+                for (int z = 0; z < HJ; ++z) {
+                    const TileInfo ti = info[at * P + h0 + z];
+                    pos0[z] = ti.pos0;
+                    ks[z] = ti.ks;
+                    vs[z] = ti.vs;
+                    masked = masked || ti.pos0 + 16 > lim0;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sc[z][j][k] = 0.f;
+                }
+                const uint32_t stage = ring_at + (uint32_t)at * kStageBytes + h0 * 2 * S::kTile;
                 // scores of 16 positions (rows) and the unit's query rows (columns)
-                float sc[NT][4];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[j][k] = 0.f;
 #pragma unroll
                 for (int h = 0; h < HD / 64; ++h) {  // 64 dims at a time
-                    const uint32_t ka = (stage + (h >> 1) * 2048 + koff) ^ ((h & 1) << 6);
-                    const uint4 k0 = lds4(ka), k1 = lds4(ka + 8 * kPitch);
-                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        uint32_t a[2][4];
+                    for (int z = 0; z < HJ; ++z) {
+                        const uint32_t ka = (stage + z * 2 * S::kTile + (h >> 1) * 2048 + koff) ^ ((h & 1) << 6);
+                        const uint4 k0 = lds4(ka), k1 = lds4(ka + 8 * kPitch);
+                        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            a[v][0] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] & 0xFFFFu));
-                            a[v][1] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] & 0xFFFFu));
-                            a[v][2] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] >> 16));
-                            a[v][3] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] >> 16));
-                        }
+                        for (int t = 0; t < 2; ++t) {
+                            uint32_t a[2][4];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const uint4 q4 = NT == 1 ? qf[2 * h + t] : *reinterpret_cast<const uint4*>(qh + (8 * j + gid) * QP + 64 * h + 16 * tig + 8 * t);
-                            mma_f16_16816(sc[j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
-                            mma_f16_16816(sc[j], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
+                            for (int v = 0; v < 2; ++v) {
+                                a[v][0] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] & 0xFFFFu));
+                                a[v][1] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] & 0xFFFFu));
+                                a[v][2] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] >> 16));
+                                a[v][3] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] >> 16));
+                            }
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {
+                                const uint4 q4 = NT == 1 ? qf[2 * h + t] : *reinterpret_cast<const uint4*>(qh + (8 * j + gid) * QP + 64 * h + 16 * tig + 8 * t);
+                                mma_f16_16816(sc[z][j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
+                                mma_f16_16816(sc[z][j], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
+                            }
                         }
                     }
                 }
                 // s - m; masked positions -inf
-                const bool masked = pos0 + 16 > lim0;  // (a limit per row matters)
-                float x[NT][4], top = -INFINITY;
+                float top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int z = 0; z < HJ; ++z)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = hf[j][e] * kscale;
-                        x[j][e] = fmaf(sc[j][e], f, -mr[j][e]);
-                        x[j][2 + e] = fmaf(sc[j][2 + e], f, -mr[j][e]);
-                    }
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float f = hf[j][e] * ks[z];
+                            x[z][j][e] = fmaf(sc[z][j][e], f, -mr[j][e]);
+                            x[z][j][2 + e] = fmaf(sc[z][j][2 + e], f, -mr[j][e]);
+                        }
                 if (masked)
 #pragma unroll
+                    for (int z = 0; z < HJ; ++z)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int lim = lims[8 * j + 2 * tig + e];
+                                if (pos0[z] + pos_of<HD>(gid) >= lim) x[z][j][e] = -INFINITY;
+                                if (pos0[z] + pos_of<HD>(gid) + 8 >= lim) x[z][j][2 + e] = -INFINITY;
+                            }
+#pragma unroll
+                for (int z = 0; z < HJ; ++z)
+#pragma unroll
                     for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int lim = lims[8 * j + 2 * tig + e];
-                            if (pos0 + pos_of<HD>(gid) >= lim) x[j][e] = -INFINITY;
-                            if (pos0 + pos_of<HD>(gid) + 8 >= lim) x[j][2 + e] = -INFINITY;
-                        }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
-                float ratio = 1.f, wmul = 1.f;
-                if (vscale != vcur) {
-                    // units: the block's v_scale, but never more than 2^90 below the largest so
-                    // far (the sums would overflow); a zero scale keeps the unit, weighs nothing
-                    if (vscale == 0.f) {
-                        wmul = 0.f;
-                    } else {
-                        vmax = fmaxf(vmax, vscale);
-                        const float unit = fmaxf(vscale, vmax * 8.077935669463161e-28f);
-                        wmul = vscale / unit;
-                        ratio = vcur / unit;
-                        vcur = unit;
-                    }
-                }
-                if (__any_sync(0xffffffffu, top > kRaise)) {
+                        top = fmaxf(top, fmaxf(fmaxf(x[z][j][0], x[z][j][1]), fmaxf(x[z][j][2], x[z][j][3])));
+                if (__any_sync(0xffffffffu, top > kRaise)) {  // a new reference for every row
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float f = hf[j][e] * kscale;
-                            const bool m0 = x[j][e] == -INFINITY, m1 = x[j][2 + e] == -INFINITY;
-                            float m = fmaxf(m0 ? -INFINITY : sc[j][e] * f, m1 ? -INFINITY : sc[j][2 + e] * f);
+                            float m = -INFINITY;
+#pragma unroll
+                            for (int z = 0; z < HJ; ++z) {
+                                const float f = hf[j][e] * ks[z];
+                                if (x[z][j][e] != -INFINITY) m = fmaxf(m, sc[z][j][e] * f);
+                                if (x[z][j][2 + e] != -INFINITY) m = fmaxf(m, sc[z][j][2 + e] * f);
+                            }
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                             const float mn = fmaxf(mr[j][e], m);
                             const float al = mr[j][e] == -INFINITY ? 0.f : ex2(mr[j][e] - mn);
                             mr[j][e] = mn;
                             l[j][e] *= al;
-                            x[j][e] = m0 ? -INFINITY : fmaf(sc[j][e], f, -mn);
-                            x[j][2 + e] = m1 ? -INFINITY : fmaf(sc[j][2 + e], f, -mn);
-                            const float by = al * ratio;
+#pragma unroll
+                            for (int z = 0; z < HJ; ++z) {
+                                const float f = hf[j][e] * ks[z];
+                                if (x[z][j][e] != -INFINITY) x[z][j][e] = fmaf(sc[z][j][e], f, -mn);
+                                if (x[z][j][2 + e] != -INFINITY) x[z][j][2 + e] = fmaf(sc[z][j][2 + e], f, -mn);
+                            }
 #pragma unroll
                             for (int dt = 0; dt < DT; ++dt) {
-                                acc[dt][j][e] *= by;
-                                acc[dt][j][2 + e] *= by;
+                                acc[dt][j][e] *= al;
+                                acc[dt][j][2 + e] *= al;
                             }
                         }
-                } else if (ratio != 1.f) {
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[dt][j][k] *= ratio;
                 }
-                // weights: summed in fp32, rounded to f16 for the product, packed per position and
-                // transposed into its B fragments
-                uint32_t bp[NT][2];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    uint32_t hw[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float w0 = ex2(x[j][e]), w1 = ex2(x[j][2 + e]);
-                        x[j][e] = w0 + w1;
-                        l[j][e] += x[j][e];
-                        if (wmul != 1.f) w0 *= wmul, w1 *= wmul;
-                        hw[e] = pack_f16x2(w0, w1);
-                    }
-                    bp[j][0] = transpose8(__byte_perm(hw[0], hw[1], 0x5410));
-                    bp[j][1] = transpose8(__byte_perm(hw[0], hw[1], 0x7632));
-                }
-                if (!SPARSE && p.a.out_mass) {
-                    // the tile's sum of weights per row: 2 NT values summed over the 8 lanes of a
-                    // column, halving what a lane carries at each step; value v ends in lanes gid
-                    // with gid % (2 NT) = v
-                    float v[2 * NT], m[2 * NT];
-#pragma unroll
-                    for (int k = 0; k < 2 * NT; ++k) v[k] = x[k >> 1][k & 1], m[k] = mr[k >> 1][k & 1];
-#pragma unroll
-                    for (int w = NT, o = 4 * NT; w; w >>= 1, o >>= 1) {
-                        const bool hi = lane & o;
-#pragma unroll
-                        for (int k = 0; k < w; ++k) {
-                            const float give = hi ? v[k] : v[k + w];
-                            v[k] = (hi ? v[k + w] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
-                            m[k] = hi ? m[k + w] : m[k];
-                        }
-                    }
-#pragma unroll
-                    for (int o = 8 * NT; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-                    const int k = gid & (2 * NT - 1), r = 8 * (k >> 1) + 2 * tig + (k & 1);
-                    if (gid < 2 * NT && r < nrows)
-                        mass_at[(int64_t)tile * mass_pitch + r] = v[0] > 0.f ? m[0] + log2f(v[0]) : v[0] != v[0] ? v[0] : -INFINITY;
-                }
-                // V^T (A) . W^T (B) over 16 positions: a lane holds kCols columns from col_of(gid)
-                // on of four positions; tile dt has column 2 dt of them in row gid, 2 dt + 1 in row
-                // gid + 8
-                const int vpos[4] = {pos_of<HD>(2 * tig), pos_of<HD>(2 * tig + 1), pos_of<HD>(2 * tig) + 8, pos_of<HD>(2 * tig + 1) + 8};
-#pragma unroll
-                for (int h = 0; h < (HD + 127) / 128; ++h) {
-                    uint32_t y[4][kWords];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t va = stage + S::kTile + h * 2048 + (k & 1 ? voff1 : voff0) + (k >> 1) * 8 * kPitch;
-                        if constexpr (HD == 64) {
-                            const uint2 v = lds2(va);
-                            y[k][0] = v.x, y[k][1] = v.y;
+                for (int z = 0; z < HJ; ++z) {
+                    float wmul = 1.f;
+                    if (vs[z] != vcur && pos0[z] != kNowhere) {
+                        // units: the block's v_scale, but never more than 2^90 below the largest so
+                        // far (the sums would overflow); a zero scale keeps the unit, weighs nothing
+                        if (vs[z] == 0.f) {
+                            wmul = 0.f;
                         } else {
-                            const uint4 v = lds4(va);
-                            y[k][0] = v.x, y[k][1] = v.y, y[k][2] = v.z, y[k][3] = v.w;
-                        }
-                    }
-                    // In a masked tile rows past the end are zeroed (0 * NaN is NaN), and NaN codes
-                    // of positions that only some rows see are taken out and given back to those
-                    int nan_at[kWords][4];
-                    bool nan_any = false;
-                    if (masked) {
+                            vmax = fmaxf(vmax, vs[z]);
+                            const float unit = fmaxf(vs[z], vmax * 8.077935669463161e-28f);
+                            wmul = vs[z] / unit;
+                            const float ratio = vcur / unit;
+                            vcur = unit;
 #pragma unroll
-                        for (int w = 0; w < kWords; ++w)
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) nan_at[w][d] = 0x7fffffff;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int w = 0; w < kWords; ++w) {
-                                if (pos0 + vpos[k] >= vlim) y[k][w] = 0;
-                                const uint32_t isn = __vcmpeq4(y[k][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                nan_any = nan_any || isn;
-#pragma unroll
-                                for (int d = 0; d < 4; ++d)
-                                    if ((isn >> (8 * d)) & 1u) nan_at[w][d] = min(nan_at[w][d], pos0 + vpos[k]);
-                                y[k][w] &= ~isn;
-                            }
-                        nan_any = __any_sync(0xffffffffu, nan_any);
-                    }
-#pragma unroll
-                    for (int w = 0; w < kWords; ++w)
-#pragma unroll
-                        for (int u2 = 0; u2 < 2; ++u2) {
-                            const uint32_t lo = __byte_perm(y[0][w], y[1][w], u2 ? 0x7362 : 0x5140);
-                            const uint32_t hi = __byte_perm(y[2][w], y[3][w], u2 ? 0x7362 : 0x5140);
-                            const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)(lo & 0xFFFFu)), a1 = e4m3x2_to_f16x2((uint16_t)(lo >> 16));
-                            const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)(hi & 0xFFFFu)), a3 = e4m3x2_to_f16x2((uint16_t)(hi >> 16));
-#pragma unroll
-                            for (int j = 0; j < NT; ++j) mma_f16_16816(acc[8 * h + 2 * w + u2][j], a0, a1, a2, a3, bp[j][0], bp[j][1]);
-                        }
-                    if (nan_any) {
-#pragma unroll
-                        for (int w = 0; w < kWords; ++w)
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                int at4 = nan_at[w][d];
-                                at4 = min(at4, __shfl_xor_sync(0xffffffffu, at4, 1));
-                                at4 = min(at4, __shfl_xor_sync(0xffffffffu, at4, 2));
+                            for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
                                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                                    for (int e = 0; e < 2; ++e)
-                                        if (at4 < lims[8 * j + 2 * tig + e]) acc[8 * h + 2 * w + d / 2][j][2 * (d & 1) + e] = __uint_as_float(0x7fc00000u);
+                                    for (int k = 0; k < 4; ++k) acc[dt][j][k] *= ratio;
+                        }
+                    }
+                    // weights: summed in fp32, rounded to f16 for the product, packed per position
+                    // and transposed into its B fragments
+                    uint32_t bp[NT][2];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        uint32_t hw[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float w0 = ex2(x[z][j][e]), w1 = ex2(x[z][j][2 + e]);
+                            x[z][j][e] = w0 + w1;
+                            l[j][e] += x[z][j][e];
+                            if (wmul != 1.f) w0 *= wmul, w1 *= wmul;
+                            hw[e] = pack_f16x2(w0, w1);
+                        }
+                        bp[j][0] = transpose8(__byte_perm(hw[0], hw[1], 0x5410));
+                        bp[j][1] = transpose8(__byte_perm(hw[0], hw[1], 0x7632));
+                    }
+                    const int tile = step * P + h0 + z;
+                    if (!SPARSE && p.a.out_mass && (P == 1 || tile < sw.tiles)) {
+                        // the tile's sum of weights per row: 2 NT values summed over the 8 lanes of
+                        // a column, halving what a lane carries at each step; value v ends in lanes
+                        // gid with gid % (2 NT) = v
+                        float v[2 * NT], m[2 * NT];
+#pragma unroll
+                        for (int k = 0; k < 2 * NT; ++k) v[k] = x[z][k >> 1][k & 1], m[k] = mr[k >> 1][k & 1];
+#pragma unroll
+                        for (int w = NT, o = 4 * NT; w; w >>= 1, o >>= 1) {
+                            const bool hi = lane & o;
+#pragma unroll
+                            for (int k = 0; k < w; ++k) {
+                                const float give = hi ? v[k] : v[k + w];
+                                v[k] = (hi ? v[k + w] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+                                m[k] = hi ? m[k + w] : m[k];
+                            }
+                        }
+#pragma unroll
+                        for (int o = 8 * NT; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                        const int k = gid & (2 * NT - 1), r = 8 * (k >> 1) + 2 * tig + (k & 1);
+                        if (gid < 2 * NT && r < nrows)
+                            mass_at[(int64_t)tile * mass_pitch + r] = v[0] > 0.f ? m[0] + log2f(v[0]) : v[0] != v[0] ? v[0] : -INFINITY;
+                    }
+                    if (pos0[z] == kNowhere) continue;  // nothing was read (the stage holds other bytes)
+                    // V^T (A) . W^T (B) over 16 positions: a lane holds kWords words of columns from
+                    // col_of(gid) on of four positions; tile dt has column 2 dt of them in row gid,
+                    // 2 dt + 1 in row gid + 8
+#pragma unroll
+                    for (int h = 0; h < (HD + 127) / 128; ++h) {
+                        uint32_t y[4][kWords];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t va = stage + z * 2 * S::kTile + S::kTile + h * 2048 + (k & 1 ? voff1 : voff0) + (k >> 1) * 8 * kPitch;
+                            if constexpr (HD == 64) {
+                                const uint2 v = lds2(va);
+                                y[k][0] = v.x, y[k][1] = v.y;
+                            } else {
+                                const uint4 v = lds4(va);
+                                y[k][0] = v.x, y[k][1] = v.y, y[k][2] = v.z, y[k][3] = v.w;
+                            }
+                        }
+                        // In a masked tile rows past the end are zeroed (0 * NaN is NaN), and NaN
+                        // codes are taken out and given back to the rows that see them: the first
+                        // position that has one, per column
+                        bool nan_any = false;
+                        if (masked) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w) {
+                                    if (pos0[z] + pos_of<HD>(2 * tig + (k & 1)) + 8 * (k >> 1) >= vlim) y[k][w] = 0;
+                                    nan_any = nan_any || __vcmpeq4(y[k][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                }
+                            nan_any = __any_sync(0xffffffffu, nan_any);
+                            if (nan_any) {
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w) {
+                                    uint32_t isn[4];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        isn[k] = __vcmpeq4(y[k][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                        y[k][w] &= ~isn[k];
+                                    }
+#pragma unroll
+                                    for (int d = 0; d < 4; ++d) {
+                                        int first_at = 0x7fffffff;
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k)
+                                            if ((isn[k] >> (8 * d)) & 1u)
+                                                first_at = min(first_at, pos0[z] + pos_of<HD>(2 * tig + (k & 1)) + 8 * (k >> 1));
+                                        first_at = min(first_at, __shfl_xor_sync(0xffffffffu, first_at, 1));
+                                        first_at = min(first_at, __shfl_xor_sync(0xffffffffu, first_at, 2));
+#pragma unroll
+                                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                            for (int e = 0; e < 2; ++e)
+                                                if (first_at < lims[8 * j + 2 * tig + e])
+                                                    acc[8 * h + 2 * w + d / 2][j][2 * (d & 1) + e] = __uint_as_float(0x7fc00000u);
+                                    }
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                            for (int u2 = 0; u2 < 2; ++u2) {
+                                const uint32_t lo = __byte_perm(y[0][w], y[1][w], u2 ? 0x7362 : 0x5140);
+                                const uint32_t hi = __byte_perm(y[2][w], y[3][w], u2 ? 0x7362 : 0x5140);
+                                const uint32_t a0 = e4m3x2_to_f16x2((uint16_t)(lo & 0xFFFFu)), a1 = e4m3x2_to_f16x2((uint16_t)(lo >> 16));
+                                const uint32_t a2 = e4m3x2_to_f16x2((uint16_t)(hi & 0xFFFFu)), a3 = e4m3x2_to_f16x2((uint16_t)(hi >> 16));
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) mma_f16_16816(acc[8 * h + 2 * w + u2][j], a0, a1, a2, a3, bp[j][0], bp[j][1]);
                             }
                     }
                 }
-            } else if (!SPARSE && p.a.out_mass) {
-                for (int r = lane; r < nrows; r += 32) mass_at[(int64_t)tile * mass_pitch + r] = -INFINITY;
             }
             __syncwarp();  // everyone is done with the stage
             issue();
@@ -709,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             }
         }
         if (warp == 0) {
-            const bool whole = t0 == 0 && t1 == sw.tiles;
+            const bool whole = t0 == 0 && t1 == sw.steps;
             float* slot = p.parts + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * (R * (HD + 4));
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -717,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 for (int e = 0; e < 2; ++e) {
                     const int r = 8 * j + 2 * tig + e;
                     if (r >= nrows) continue;
-                    const int tok = (row0 + r) / p.group, i = (row0 + r) - tok * p.group;
+                    const int tok = token_of(r), i = (row0 + r) - tok * p.group;
                     const int64_t row = ((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i;
                     const bool some = !(l[j][e] <= 0.f);
                     const float inv = some ? 1.f / l[j][e] : 0.f;
@@ -760,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 // nothing. One warp or four (they split the parts) per query row.
 template <int HD, int NT, bool SPARSE, int WPR>
 __global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int R = 8 * NT, V = HD / 32;
+    constexpr int R = 8 * NT, V = HD / 32, P = Shape<HD, NT>::P;
     __shared__ float sums[4][HD];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + warp;
@@ -769,7 +824,7 @@ __global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_const
     const int64_t bt = row / p.a.nq;
     const int b = (int)(bt / p.t.T), tok = (int)(bt % p.t.T), head = (int)(row % p.a.nq);
     if (b >= p.t.B) return;
-    const SeqWork sw = seq_work<NT, SPARSE>(p, b);
+    const SeqWork sw = seq_work<NT, SPARSE, P>(p, b);
     if (tok >= sw.q) return;
     const int g = head / p.group;
     const int r_abs = SPARSE ? head - g * p.group : tok * p.group + head - g * p.group;
@@ -777,9 +832,9 @@ __global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_const
     float M = -INFINITY, L = 0.f, a[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a[v] = 0.f;
-    if (sw.tiles > 0) {
+    if (sw.steps > 0) {
         const int per = *p.per, base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
-        const int c0 = base / per, c1 = (base + sw.tiles - 1) / per;
+        const int c0 = base / per, c1 = (base + sw.steps - 1) / per;
         if (c0 == c1) return;  // finished by one CTA
         const float* parts = p.parts;
         // in CTA c0 the unit is the last (slot 1) unless it is also the first; in later ones the first
@@ -838,7 +893,7 @@ __global__ void __launch_bounds__(256) block_mass_kernel(const __grid_constant__
     const int b = blockIdx.y, t = threadIdx.x & 31, gs = threadIdx.x >> 5;
     const int tile = (int)blockIdx.x * 32 + t;
     pdl_wait();
-    const SeqWork w = seq_work<1, false>(p, b);
+    const SeqWork w = seq_work<1, false, 1>(p, b);
     const int pitch = (int)p.t.T * p.group, rows = w.q * p.group;
     float sum = 0.f;
     if (tile < w.tiles)
@@ -986,7 +1041,8 @@ cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const Bl
     // tiles of all units on one line: 32-bit indices
     if ((double)l.units * (double)(sparse ? (int64_t)a.n_sel * (c.bs / 16) : l.tiles) >= 2147483648.0) return cudaErrorInvalidValue;
     AttnParams p{c, t, a, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int32_t*>(ws),
-                 reinterpret_cast<int32_t*>(ws + l.base), c.bs == 16 ? 0 : c.bs == 32 ? 1 : 2, reinterpret_cast<float*>(ws + l.parts),
+                 reinterpret_cast<int32_t*>(ws + l.base), c.bs == 16 ? 0 : c.bs == 32 ? 1 : 2,
+                 ((1u << 20) + (uint32_t)(a.nq / c.nkv) - 1u) / (uint32_t)(a.nq / c.nkv), reinterpret_cast<float*>(ws + l.parts),
                  reinterpret_cast<float*>(ws + l.row_lse), reinterpret_cast<float*>(ws + l.tile_lse)};
     int dev = 0, sms = 148;
     cudaError_t e;
