@@ -6,8 +6,10 @@
 // with any reference m: a running one, raised only when a score exceeds it by more than 8
 // binades (weights stay below 2^8, inside f16), so that most tiles need no maximum, no shuffle
 // and no rescaling, just one vote. A block's v_scale is not folded into the weights (they would
-// lose f16 bits): the accumulators are held in units of the current block's v_scale and change
-// units when it changes, an exact shift for powers of two.
+// lose f16 bits where scales lie far apart): the accumulators are held in units of an earlier
+// block's v_scale, weights are multiplied by v_scale / unit before they are rounded, and the
+// unit moves when that leaves [2^-10, 2^6] (weights below 2^14 fit f16, and what a rounding to
+// its smallest steps takes, 2^-25, is 2^-15 of the block's largest weight at most).
 //
 // Work: the cache is read in tiles of 16 positions, each inside one block. A unit is a kv head
 // of a sequence with up to 8 NT of its T (nq / nkv) query rows (for listed blocks: of a
@@ -96,8 +98,9 @@ template <int HD, int NT>
 struct Shape {
     static constexpr int kTile = 16 * HD;                        // bytes of K (or V) of a tile
     static constexpr int P = HD == 256 ? 1 : 2;                  // tiles per step
-    static constexpr int kJoint = HD == 256 || NT == 4 ? 1 : P;  // of them worked on together (registers)
-    static constexpr int kPerSm = HD == 256 || NT >= 2 ? 2 : 3;  // CTAs per SM
+    // of them worked on together, and CTAs per SM: as the accumulators leave registers
+    static constexpr int kJoint = HD == 64 ? (NT <= 2 ? P : 1) : HD == 128 ? (NT <= 2 ? P : 1) : 1;
+    static constexpr int kPerSm = HD == 64 ? (NT <= 5 ? 3 : 2) : HD == 128 ? (NT <= 1 ? 3 : 2) : 2;
     static constexpr int kQPitch = HD + 8;                       // f16 elements
     static constexpr int kRows = 8 * NT;
     static constexpr size_t kFixed = (size_t)HD * NT * 64           // two warps' accumulators
@@ -127,6 +130,33 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
 }
 // Transpose of an 8 x 8 matrix of 16-bit values in the mma fragment layout.
@@ -202,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     volatile int* abort = reinterpret_cast<volatile int*>(redl + kWarps * R);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_launch_dependents();
     const uint32_t ring_at = smem_u32(ring);
     if (ring_at & 1023u) {  // (the swizzled copies need it; dynamic shared memory starts there)
         if (tid == 0) raise_flag(p.t.dev_err, DEVFLAG_TIMEOUT);
@@ -213,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     mbar_fence_init();
     __syncthreads();
     pdl_wait();  // everything below reads or writes memory that earlier kernels may still use
+    pdl_launch_dependents();  // (the next kernel may read what was there before this one)
 
     // this CTA's stretch of the line: `stretch` steps from `beg` on, and the sequence, unit and
     // step it starts with (every warp for itself, 32 sequences at a time)
@@ -336,12 +366,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         if (lane == 0) mbar_arrive_expect_tx(&full[at], (uint32_t)__popc((ah_read >> (ah_n * P)) & ((1u << P) - 1u)) * 2u * S::kTile);
         __syncwarp();
         if (lane / P == ah_n) {
-            TileInfo ti;
-            ti.pos0 = ah_pos;
-            ti.ks = ah_ks;
-            ti.vs = ah_vs;
-            ti.pad = 0;
-            info[at * P + lane % P] = ti;
             if (ah_blk >= 0) {
                 uint8_t* kd = ring + (size_t)at * kStageBytes + (lane % P) * 2 * S::kTile;
                 const int row = ah_pos & ((16 << p.tile_shift) - 1);
@@ -352,6 +376,12 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     load_tile(kd + S::kTile + x * 16, &vmap, x, row, g, ah_blk, &full[at]);
                 }
             }
+            TileInfo ti;
+            ti.pos0 = ah_pos;
+            ti.ks = ah_ks;
+            ti.vs = ah_vs;
+            ti.pad = 0;
+            info[at * P + lane % P] = ti;
         }
         if (++ist == ST) ist = 0;
         if (++ah_n == ah_cnt) {
@@ -428,16 +458,14 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
             for (int c = 0; c < KC / 2; ++c)
                 qf[c] = *reinterpret_cast<const uint4*>(qh + gid * QP + 64 * (c >> 1) + 16 * tig + 8 * (c & 1));
-        float hf[NT][2], mr[NT][2], l[NT][2], acc[DT][NT][4];
-        float vcur = 0.f, vmax = 0.f;  // the accumulators' unit, the largest v_scale so far
+        float2 hf[NT], nm[NT], l[NT];  // rows 8 j + 2 tig, + 1: score factor, minus reference, sum
+        float acc[DT][NT][4];
+        float vcur = 0.f, vinv = 0.f, vmax = 0.f;  // the accumulators' unit, 1 over it, the largest v_scale so far
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                hf[j][e] = hfac[8 * j + 2 * tig + e];
-                mr[j][e] = -INFINITY;
-                l[j][e] = 0.f;
-            }
+            hf[j] = *reinterpret_cast<const float2*>(hfac + 8 * j + 2 * tig);
+            nm[j] = make_float2(INFINITY, INFINITY);
+            l[j] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -493,18 +521,16 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                         }
                     }
                 }
-                // s - m; masked positions -inf
-                float top = -INFINITY;
+                // s - m, (row 2 tig, row 2 tig + 1) of positions gid and gid + 8; masked ones -inf
 #pragma unroll
                 for (int z = 0; z < HJ; ++z)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float f = hf[j][e] * ks[z];
-                            x[z][j][e] = fmaf(sc[z][j][e], f, -mr[j][e]);
-                            x[z][j][2 + e] = fmaf(sc[z][j][2 + e], f, -mr[j][e]);
-                        }
+                    for (int j = 0; j < NT; ++j) {
+                        const float2 f = mul2(hf[j], make_float2(ks[z], ks[z]));
+                        const float2 x0 = fma2(make_float2(sc[z][j][0], sc[z][j][1]), f, nm[j]);
+                        const float2 x1 = fma2(make_float2(sc[z][j][2], sc[z][j][3]), f, nm[j]);
+                        x[z][j][0] = x0.x, x[z][j][1] = x0.y, x[z][j][2] = x1.x, x[z][j][3] = x1.y;
+                    }
                 if (masked)
 #pragma unroll
                     for (int z = 0; z < HJ; ++z)
@@ -516,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                                 if (pos0[z] + pos_of<HD>(gid) >= lim) x[z][j][e] = -INFINITY;
                                 if (pos0[z] + pos_of<HD>(gid) + 8 >= lim) x[z][j][2 + e] = -INFINITY;
                             }
+                float top = -INFINITY;
 #pragma unroll
                 for (int z = 0; z < HJ; ++z)
 #pragma unroll
@@ -523,41 +550,46 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                         top = fmaxf(top, fmaxf(fmaxf(x[z][j][0], x[z][j][1]), fmaxf(x[z][j][2], x[z][j][3])));
                 if (__any_sync(0xffffffffu, top > kRaise)) {  // a new reference for every row
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int j = 0; j < NT; ++j) {
+                        float nmj[2] = {nm[j].x, nm[j].y}, al[2];
+                        const float hfj[2] = {hf[j].x, hf[j].y};
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float m = -INFINITY;
 #pragma unroll
                             for (int z = 0; z < HJ; ++z) {
-                                const float f = hf[j][e] * ks[z];
+                                const float f = hfj[e] * ks[z];
                                 if (x[z][j][e] != -INFINITY) m = fmaxf(m, sc[z][j][e] * f);
                                 if (x[z][j][2 + e] != -INFINITY) m = fmaxf(m, sc[z][j][2 + e] * f);
                             }
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            const float mn = fmaxf(mr[j][e], m);
-                            const float al = mr[j][e] == -INFINITY ? 0.f : ex2(mr[j][e] - mn);
-                            mr[j][e] = mn;
-                            l[j][e] *= al;
+                            const float mn = fmaxf(-nmj[e], m);
+                            al[e] = nmj[e] == INFINITY ? 0.f : ex2(-nmj[e] - mn);
+                            nmj[e] = -mn;
 #pragma unroll
                             for (int z = 0; z < HJ; ++z) {
-                                const float f = hf[j][e] * ks[z];
+                                const float f = hfj[e] * ks[z];
                                 if (x[z][j][e] != -INFINITY) x[z][j][e] = fmaf(sc[z][j][e], f, -mn);
                                 if (x[z][j][2 + e] != -INFINITY) x[z][j][2 + e] = fmaf(sc[z][j][2 + e], f, -mn);
                             }
 #pragma unroll
                             for (int dt = 0; dt < DT; ++dt) {
-                                acc[dt][j][e] *= al;
-                                acc[dt][j][2 + e] *= al;
+                                acc[dt][j][e] *= al[e];
+                                acc[dt][j][2 + e] *= al[e];
                             }
                         }
+                        nm[j] = make_float2(nmj[0], nmj[1]);
+                        l[j] = mul2(l[j], make_float2(al[0], al[1]));
+                    }
                 }
 #pragma unroll
                 for (int z = 0; z < HJ; ++z) {
-                    float wmul = 1.f;
-                    if (vs[z] != vcur && pos0[z] != kNowhere) {
-                        // units: the block's v_scale, but never more than 2^90 below the largest so
-                        // far (the sums would overflow); a zero scale keeps the unit, weighs nothing
+                    // the block's v_scale over the accumulators' unit
+                    float wmul = vs[z] * vinv;
+                    if (!(wmul >= 9.765625e-4f && wmul <= 64.f) && pos0[z] != kNowhere) {
+                        // a new unit: the block's v_scale, but never more than 2^90 below the
+                        // largest so far (the sums would overflow); a zero scale weighs nothing
                         if (vs[z] == 0.f) {
                             wmul = 0.f;
                         } else {
@@ -566,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                             wmul = vs[z] / unit;
                             const float ratio = vcur / unit;
                             vcur = unit;
+                            vinv = 1.f / unit;
 #pragma unroll
                             for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -574,46 +607,54 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                                     for (int k = 0; k < 4; ++k) acc[dt][j][k] *= ratio;
                         }
                     }
-                    // weights: summed in fp32, rounded to f16 for the product, packed per position
-                    // and transposed into its B fragments
+                    vmax = fmaxf(vmax, vs[z]);
+                    // weights: summed in fp32, rounded to f16 for the product and transposed into
+                    // its B fragments (rows to columns)
                     uint32_t bp[NT][2];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        uint32_t hw[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float w0 = ex2(x[z][j][e]), w1 = ex2(x[z][j][2 + e]);
-                            x[z][j][e] = w0 + w1;
-                            l[j][e] += x[z][j][e];
-                            if (wmul != 1.f) w0 *= wmul, w1 *= wmul;
-                            hw[e] = pack_f16x2(w0, w1);
-                        }
-                        bp[j][0] = transpose8(__byte_perm(hw[0], hw[1], 0x5410));
-                        bp[j][1] = transpose8(__byte_perm(hw[0], hw[1], 0x7632));
+                        const float2 w0 = make_float2(ex2(x[z][j][0]), ex2(x[z][j][1])), w1 = make_float2(ex2(x[z][j][2]), ex2(x[z][j][3]));
+                        const float2 ws = add2(w0, w1);
+                        x[z][j][0] = ws.x, x[z][j][1] = ws.y;
+                        l[j] = add2(l[j], ws);
+                        const float2 wm = make_float2(wmul, wmul), u0 = mul2(w0, wm), u1 = mul2(w1, wm);
+                        bp[j][0] = transpose8(pack_f16x2(u0.x, u0.y));
+                        bp[j][1] = transpose8(pack_f16x2(u1.x, u1.y));
                     }
                     const int tile = step * P + h0 + z;
                     if (!SPARSE && p.a.out_mass && (P == 1 || tile < sw.tiles)) {
-                        // the tile's sum of weights per row: 2 NT values summed over the 8 lanes of
-                        // a column, halving what a lane carries at each step; value v ends in lanes
-                        // gid with gid % (2 NT) = v
-                        float v[2 * NT], m[2 * NT];
+                        // the tile's sum of weights per row: 2 NT values (padded to VP) summed over
+                        // the 8 lanes of a column; each step halves what a lane carries
+                        constexpr int VP = NT <= 1 ? 2 : NT <= 2 ? 4 : NT <= 4 ? 8 : 16;
+                        float v[VP], m[VP];
 #pragma unroll
-                        for (int k = 0; k < 2 * NT; ++k) v[k] = x[z][k >> 1][k & 1], m[k] = mr[k >> 1][k & 1];
+                        for (int k = 0; k < VP; ++k) {
+                            v[k] = k < 2 * NT ? x[z][k >> 1][k & 1] : 0.f;
+                            m[k] = k >= 2 * NT ? 0.f : k & 1 ? nm[k >> 1].y : nm[k >> 1].x;
+                        }
+                        int k0 = 0;  // the value in v[0]
 #pragma unroll
-                        for (int w = NT, o = 4 * NT; w; w >>= 1, o >>= 1) {
+                        for (int o = 16, n = VP; o >= 4; o >>= 1) {
                             const bool hi = lane & o;
+                            n >>= 1;
+                            if (n) {
+                                if (hi) k0 += n;
 #pragma unroll
-                            for (int k = 0; k < w; ++k) {
-                                const float give = hi ? v[k] : v[k + w];
-                                v[k] = (hi ? v[k + w] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
-                                m[k] = hi ? m[k + w] : m[k];
+                                for (int k = 0; k < n; ++k) {
+                                    const float give = hi ? v[k] : v[k + n];
+                                    v[k] = (hi ? v[k + n] : v[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+                                    m[k] = hi ? m[k + n] : m[k];
+                                }
+                            } else {
+                                v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
                             }
                         }
 #pragma unroll
-                        for (int o = 8 * NT; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-                        const int k = gid & (2 * NT - 1), r = 8 * (k >> 1) + 2 * tig + (k & 1);
-                        if (gid < 2 * NT && r < nrows)
-                            mass_at[(int64_t)tile * mass_pitch + r] = v[0] > 0.f ? m[0] + log2f(v[0]) : v[0] != v[0] ? v[0] : -INFINITY;
+                        for (int k = 0; k < (VP > 8 ? VP / 8 : 1); ++k) {
+                            const int r = 8 * ((k0 + k) >> 1) + 2 * tig + ((k0 + k) & 1);
+                            if (r < nrows)  // (several lanes may hold the same value)
+                                mass_at[(int64_t)tile * mass_pitch + r] = v[k] > 0.f ? lg2(v[k]) - m[k] : v[k] != v[k] ? v[k] : -INFINITY;
+                        }
                     }
                     if (pos0[z] == kNowhere) continue;  // nothing was read (the stage holds other bytes)
                     // V^T (A) . W^T (B) over 16 positions: a lane holds kWords words of columns from
@@ -697,12 +738,18 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         }
 
         // join the four warps (fixed order): the largest reference M, everything times 2^(m - M)
+        float mr[NT][2], ls[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            mr[j][0] = -nm[j].x, mr[j][1] = -nm[j].y;
+            ls[j][0] = l[j].x, ls[j][1] = l[j].y;
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], o);
+                for (int o = 4; o < 32; o <<= 1) ls[j][e] += __shfl_xor_sync(0xffffffffu, ls[j][e], o);
         if (gid == 0)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -710,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 for (int e = 0; e < 2; ++e) {
                     const int r = warp * R + 8 * j + 2 * tig + e;
                     redm[r] = mr[j][e];
-                    redl[r] = l[j][e];
+                    redl[r] = ls[j][e];
                 }
         __syncthreads();
 #pragma unroll
@@ -729,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     L += f * redl[w * R + r];
                 }
                 mr[j][e] = M;
-                l[j][e] = L;
+                ls[j][e] = L;
                 const float by = mine * vcur;
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) {
@@ -774,8 +821,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     if (r >= nrows) continue;
                     const int tok = token_of(r), i = (row0 + r) - tok * p.group;
                     const int64_t row = ((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i;
-                    const bool some = !(l[j][e] <= 0.f);
-                    const float inv = some ? 1.f / l[j][e] : 0.f;
+                    const bool some = !(ls[j][e] <= 0.f);
+                    const float inv = some ? 1.f / ls[j][e] : 0.f;
 #pragma unroll
                     for (int dt = 0; dt < DT; dt += 4) {  // 8 columns
                         const int d = (dt >> 3) * 128 + col_of<HD>(gid) + 2 * (dt & 7);
@@ -794,12 +841,12 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     }
                     if (gid == 0) {
                         if (whole) {
-                            const float lse2 = some ? mr[j][e] + log2f(l[j][e]) : -INFINITY;
+                            const float lse2 = some ? mr[j][e] + log2f(ls[j][e]) : -INFINITY;
                             if (p.a.out_lse) p.a.out_lse[row] = lse2 * kLn2;
                             if (!SPARSE && p.a.out_mass) p.row_lse[((int64_t)b * p.c.nkv + g) * mass_pitch + row0 + r] = lse2;
                         } else {
                             slot[r] = mr[j][e];
-                            slot[R + r] = l[j][e];
+                            slot[R + r] = ls[j][e];
                         }
                     }
                 }
@@ -812,23 +859,28 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 }
 
 // Joins the partial sums of the units that several CTAs share, and writes the rows that see
-// nothing. One warp or four (they split the parts) per query row.
+// nothing. WPR warps per query row split the parts, each with all its loads in flight at once.
 template <int HD, int NT, bool SPARSE, int WPR>
-__global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int R = 8 * NT, V = HD / 32, P = Shape<HD, NT>::P;
-    __shared__ float sums[4][HD];
+__global__ void __launch_bounds__(32 * (WPR > 4 ? WPR : 4)) block_attn_join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int R = 8 * NT, V = HD / 32, P = Shape<HD, NT>::P, NW = WPR > 4 ? WPR : 4, K = 8;
+    __shared__ __align__(16) float sums[WPR > 1 ? WPR : 1][HD];
+    __shared__ float ms[WPR], ls[WPR];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = WPR == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + warp;
-    const int wr = WPR == 4 ? warp : 0;
-    pdl_wait();
+    const int64_t row = (int64_t)blockIdx.x * (NW / WPR) + warp / WPR;
+    const int wr = warp % WPR;
     const int64_t bt = row / p.a.nq;
     const int b = (int)(bt / p.t.T), tok = (int)(bt % p.t.T), head = (int)(row % p.a.nq);
-    if (b >= p.t.B) return;
+    if (b >= p.t.B) {
+        pdl_wait();
+        return;
+    }
+    // (the lengths were written before the kernel that lets this one start)
     const SeqWork sw = seq_work<NT, SPARSE, P>(p, b);
-    if (tok >= sw.q) return;
-    const int g = head / p.group;
+    const int g = (int)(((uint32_t)head * p.group_inv) >> 20);
     const int r_abs = SPARSE ? head - g * p.group : tok * p.group + head - g * p.group;
     const int part = SPARSE ? tok : r_abs / R, r = SPARSE ? r_abs : r_abs - part * R;
+    pdl_wait();
+    if (tok >= sw.q) return;
     float M = -INFINITY, L = 0.f, a[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a[v] = 0.f;
@@ -836,41 +888,73 @@ __global__ void __launch_bounds__(128) block_attn_join_kernel(const __grid_const
         const int per = *p.per, base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
         const int c0 = base / per, c1 = (base + sw.steps - 1) / per;
         if (c0 == c1) return;  // finished by one CTA
-        const float* parts = p.parts;
         // in CTA c0 the unit is the last (slot 1) unless it is also the first; in later ones the first
         auto slot = [&](int c) {
-            return parts + (int64_t)(c * 2 + (c == c0 && base != c0 * per ? 1 : 0)) * (R * (HD + 4));
+            return p.parts + (int64_t)(c * 2 + (c == c0 && base != c0 * per ? 1 : 0)) * (R * (HD + 4));
         };
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[r]);
+        for (int k0 = c0 + wr; k0 <= c1; k0 += K * WPR) {
+            float m[K], l[K], x[K][V];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            const float* s = slot(c);
-            const float f = s[r] == -INFINITY ? 0.f : ex2(s[r] - M);
-            L += f * s[R + r];
+            for (int k = 0; k < K; ++k) {
+                const int c = k0 + k * WPR;
+                m[k] = -INFINITY;
+                l[k] = 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[k][v] = 0.f;
+                if (c <= c1) {
+                    const float* s = slot(c);
+                    m[k] = s[r];
+                    l[k] = s[R + r];
+                    const float* y = s + R * 4 + r * HD + lane * V;
+                    if constexpr (V == 2) {
+                        const float2 t = *reinterpret_cast<const float2*>(y);
+                        x[k][0] = t.x, x[k][1] = t.y;
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < V; v += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(y + v);
+                            x[k][v] = t.x, x[k][v + 1] = t.y, x[k][v + 2] = t.z, x[k][v + 3] = t.w;
+                        }
+                    }
+                }
+            }
+            float mn = M;
+#pragma unroll
+            for (int k = 0; k < K; ++k) mn = fmaxf(mn, m[k]);
+            const float al = M == -INFINITY ? 0.f : ex2(M - mn);
+            L *= al;
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[v] *= al;
+            M = mn;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float f = m[k] == -INFINITY ? 0.f : ex2(m[k] - mn);
+                L += f * l[k];
+#pragma unroll
+                for (int v = 0; v < V; ++v) a[v] = fmaf(f, x[k][v], a[v]);
+            }
         }
+        if constexpr (WPR > 1) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            L += __shfl_xor_sync(0xffffffffu, L, o);
-        }
-#pragma unroll 4
-        for (int c = c0 + wr; c <= c1; c += WPR) {
-            const float* s = slot(c);
-            const float f = s[r] == -INFINITY ? 0.f : ex2(s[r] - M);
-            const float* x = s + R * 4 + r * HD + lane * V;
-#pragma unroll
-            for (int v = 0; v < V; ++v) a[v] = fmaf(f, x[v], a[v]);
-        }
-        if (WPR == 4) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) sums[warp][lane * V + v] = a[v];
+            for (int v = 0; v < V; ++v) sums[wr][lane * V + v] = a[v];
+            if (lane == 0) ms[wr] = M, ls[wr] = L;
             __syncthreads();  // (every warp of the CTA has the same row)
-            if (warp) return;
+            if (wr) return;
+            M = -INFINITY;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                a[v] = ((a[v] + sums[1][lane * V + v]) + sums[2][lane * V + v]) + sums[3][lane * V + v];
+            for (int w = 0; w < WPR; ++w) M = fmaxf(M, ms[w]);
+            L = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[v] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) {
+                const float f = ms[w] == -INFINITY ? 0.f : ex2(ms[w] - M);
+                L += f * ls[w];
+#pragma unroll
+                for (int v = 0; v < V; ++v) a[v] = fmaf(f, sums[w][lane * V + v], a[v]);
+            }
         }
-    } else if (WPR == 4 && warp) {
+    } else if (wr) {
         return;
     }
     const bool some = !(L <= 0.f);
@@ -922,9 +1006,17 @@ __global__ void __launch_bounds__(256) block_mass_kernel(const __grid_constant__
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// Row tiles of 8 NT query rows: the smallest that holds them, 32 rows at most (16 for 256-dim
-// heads, whose accumulators are twice as long).
-int pick_nt(int hd, int64_t rows) { return rows <= 8 ? 1 : rows <= 16 || hd == 256 ? 2 : 4; }
+// Query rows per unit, as 8 NT: a head's rows in as few row tiles as the accumulators allow
+// (64 rows of 64 dims, 32 of 128, 16 of 256: 128 registers), of the smallest NT that is built
+// and holds an equal share of them. (40 rows of 64 dims: one tile of NT 5 reads every code once;
+// two tiles of NT 4 took 100 us where it takes a third of that.)
+int pick_nt(int hd, int64_t rows) {
+    const int most = hd == 64 ? 8 : hd == 128 ? 4 : 2;
+    const int64_t tiles = (rows + 8 * most - 1) / (8 * most);
+    const int need = (int)((rows + 8 * tiles - 1) / (8 * tiles));
+    if (hd == 64 && need > 3) return need <= 5 ? 5 : 8;
+    return need;
+}
 
 struct Layout {
     int nt, row_tiles;
@@ -1004,17 +1096,24 @@ cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& km, const CUtens
     int grid = sms * Sh::kPerSm;
     if (grid > kMaxGrid) grid = kMaxGrid;
     if ((e = launch_after(kern, dim3((unsigned)grid), kThreads, Sh::kSmem, s, p, km, vm)) != cudaSuccess) return e;
-    // four warps per row while the rows are few (many parts each), one when they fill the GPU
+    // eight warps per row while the rows are few (many parts each), one when they fill the GPU
     const int64_t rows = (int64_t)p.t.B * p.t.T * p.a.nq;
-    if (rows <= 4096) return launch_after(block_attn_join_kernel<HD, NT, SPARSE, 4>, dim3((unsigned)rows), 128, 0, s, p);
+    if (rows <= 1024) return launch_after(block_attn_join_kernel<HD, NT, SPARSE, 8>, dim3((unsigned)rows), 256, 0, s, p);
     return launch_after(block_attn_join_kernel<HD, NT, SPARSE, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, p);
 }
 
 template <int HD, bool SPARSE>
 cudaError_t launch_attn_nt(int nt, const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
     if (nt == 1) return launch_attn<HD, 1, SPARSE>(p, km, vm, sms, s);
-    if constexpr (HD < 256 && !SPARSE)
+    if constexpr (!SPARSE && HD == 64) {
+        if (nt == 3) return launch_attn<HD, 3, SPARSE>(p, km, vm, sms, s);
+        if (nt == 5) return launch_attn<HD, 5, SPARSE>(p, km, vm, sms, s);
+        if (nt == 8) return launch_attn<HD, 8, SPARSE>(p, km, vm, sms, s);
+    }
+    if constexpr (!SPARSE && HD == 128) {
+        if (nt == 3) return launch_attn<HD, 3, SPARSE>(p, km, vm, sms, s);
         if (nt == 4) return launch_attn<HD, 4, SPARSE>(p, km, vm, sms, s);
+    }
     return launch_attn<HD, 2, SPARSE>(p, km, vm, sms, s);
 }
 
