@@ -99,8 +99,8 @@ struct Shape {
     static constexpr int kTile = 16 * HD;                        // bytes of K (or V) of a tile
     static constexpr int P = HD == 256 ? 1 : 2;                  // tiles per step
     // of them worked on together, and CTAs per SM: as the accumulators leave registers
-    static constexpr int kJoint = HD == 64 ? (NT <= 2 ? P : 1) : HD == 128 ? (NT <= 2 ? P : 1) : 1;
-    static constexpr int kPerSm = HD == 64 ? (NT <= 5 ? 3 : 2) : HD == 128 ? (NT <= 1 ? 3 : 2) : 2;
+    static constexpr int kJoint = HD < 256 && NT <= 2 ? P : 1;
+    static constexpr int kPerSm = HD == 64 ? (NT <= 2 ? 3 : 2) : HD == 128 ? (NT <= 1 ? 3 : 2) : 2;
     static constexpr int kQPitch = HD + 8;                       // f16 elements
     static constexpr int kRows = 8 * NT;
     static constexpr size_t kFixed = (size_t)HD * NT * 64           // two warps' accumulators
@@ -164,6 +164,22 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
+}
+__device__ __forceinline__ void copy4_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Arrive on `bar` (one of its expected arrivals) when this thread's earlier cp.async are done.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// mma_f16_16816 onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, int x, int row, int head, int block,
                                           uint64_t* bar) {
@@ -237,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         if (tid == 0) raise_flag(p.t.dev_err, DEVFLAG_TIMEOUT);
         return;
     }
-    if (tid < kWarps * ST) mbar_init(&full[tid], 1);
+    // arrivals: lane 0 with the tiles' bytes, and one per tile for its scales
+    if (tid < kWarps * ST) mbar_init(&full[tid], 1 + P);
     if (tid == 0) *abort = 0;
     mbar_fence_init();
     __syncthreads();
@@ -320,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     // step l / P from ah_step on; ah_n counts the steps of those that have been issued.
     Place ah = pl;
     int ah_step = ah.t0 + warp, ah_n = 0, ah_cnt = 0, ah_blk = -1, ah_pos = kNowhere;
-    float ah_ks = 0.f, ah_vs = 0.f;
     uint32_t ah_read = 0;
     bool ah_more = true;
     int ist = 0;  // the stage the next copies go to
@@ -346,14 +362,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         const bool seen = mine && lb >= 0 && pos < lim;
         ah_blk = seen ? table_block(p.t, p.c.num_blocks, ah.b, lb) : -1;
         if (seen && ah_blk < 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
-        ah_pos = kNowhere;
-        ah_ks = ah_vs = 0.f;
-        if (ah_blk >= 0) {
-            const int64_t at = (int64_t)ah_blk * p.c.nkv + g;
-            ah_ks = p.c.k_scale[at];
-            ah_vs = p.c.v_scale[at];
-            ah_pos = (int)pos;
-        }
+        ah_pos = ah_blk >= 0 ? (int)pos : kNowhere;
         ah_read = __ballot_sync(0xffffffffu, ah_blk >= 0);
     };
     auto issue = [&]() {
@@ -366,6 +375,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         if (lane == 0) mbar_arrive_expect_tx(&full[at], (uint32_t)__popc((ah_read >> (ah_n * P)) & ((1u << P) - 1u)) * 2u * S::kTile);
         __syncwarp();
         if (lane / P == ah_n) {
+            TileInfo* ti = &info[at * P + lane % P];
+            ti->pos0 = ah_pos;
             if (ah_blk >= 0) {
                 uint8_t* kd = ring + (size_t)at * kStageBytes + (lane % P) * 2 * S::kTile;
                 const int row = ah_pos & ((16 << p.tile_shift) - 1);
@@ -375,13 +386,14 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     load_tile(kd + x * 16, &kmap, x, row, g, ah_blk, &full[at]);
                     load_tile(kd + S::kTile + x * 16, &vmap, x, row, g, ah_blk, &full[at]);
                 }
+                const int64_t sc = (int64_t)ah_blk * p.c.nkv + g;
+                copy4_async(&ti->ks, p.c.k_scale + sc);
+                copy4_async(&ti->vs, p.c.v_scale + sc);
+                copies_arrive(&full[at]);
+            } else {
+                ti->ks = ti->vs = 0.f;
+                mbar_arrive(&full[at]);
             }
-            TileInfo ti;
-            ti.pos0 = ah_pos;
-            ti.ks = ah_ks;
-            ti.vs = ah_vs;
-            ti.pad = 0;
-            info[at * P + lane % P] = ti;
         }
         if (++ist == ST) ist = 0;
         if (++ah_n == ah_cnt) {
@@ -389,6 +401,24 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             look_up();
         }
     };
+    // The query rows of a unit, 16 bytes per lane and row: the first unit's are asked for before
+    // its tiles, which keep the memory busy for microseconds.
+    constexpr int LH = HD / 8, HPL = 32 / LH, NQ = (R + kWarps * HPL - 1) / (kWarps * HPL);  // lanes per row, rows per warp
+    uint4 qv[NQ];
+    auto load_q = [&]() {
+        const int row0 = SPARSE ? pl.outer * p.group : pl.inner * R, g = SPARSE ? pl.inner : pl.outer;
+        const int nrows = SPARSE ? p.group : min(R, pl.sw.q * p.group - row0);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int r = (n * kWarps + warp) * HPL + lane / LH;
+            const int tok = (int)(((uint32_t)(row0 + r) * p.group_inv) >> 20), i = (row0 + r) - tok * p.group;
+            qv[n] = make_uint4(0, 0, 0, 0);
+            if (r < nrows)
+                qv[n] = *reinterpret_cast<const uint4*>(p.a.q + ((int64_t)pl.b * p.t.T + tok) * p.a.q_stride +
+                                                        ((int64_t)g * p.group + i) * HD + 8 * (lane % LH));
+        }
+    };
+    load_q();
     look_up();
 #pragma unroll 1
     for (int i = 0; i < ST; ++i) issue();
@@ -421,14 +451,12 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         __syncthreads();  // the previous unit's rows and sums are no longer needed
         {
             // q rows in f16, each scaled by 2^e so that its largest |q| lies in [2^14, 2^15)
-            constexpr int LH = HD / 8, HPL = 32 / LH;  // lanes per row, rows per warp at a time
-            for (int r = warp * HPL + lane / LH; r < R; r += kWarps * HPL) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const int r = (n * kWarps + warp) * HPL + lane / LH;
                 const bool has = r < nrows;
-                const int tok = token_of(r), i = (row0 + r) - tok * p.group;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (has)
-                    v = *reinterpret_cast<const uint4*>(p.a.q + ((int64_t)b * p.t.T + tok) * p.a.q_stride +
-                                                        ((int64_t)g * p.group + i) * HD + 8 * (lane % LH));
+                const int tok = token_of(r);
+                const uint4 v = qv[n];
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 float mx = 0.f;
 #pragma unroll
@@ -443,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 uint32_t o4[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o4[k] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
-                *reinterpret_cast<uint4*>(qh + r * QP + 8 * (lane % LH)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-                if (lane % LH == 0) {
+                if (r < R) *reinterpret_cast<uint4*>(qh + r * QP + 8 * (lane % LH)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                if (r < R && lane % LH == 0) {
                     hfac[r] = !has ? 0.f : fin ? p.a.scale * kLog2e * down : __uint_as_float(0x7fc00000u);
                     lims[r] = has ? min(sw.len - sw.q + tok + 1, kNowhere) : kNowhere;
                 }
@@ -458,13 +486,14 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
             for (int c = 0; c < KC / 2; ++c)
                 qf[c] = *reinterpret_cast<const uint4*>(qh + gid * QP + 64 * (c >> 1) + 16 * tig + 8 * (c & 1));
-        float2 hf[NT], nm[NT], l[NT];  // rows 8 j + 2 tig, + 1: score factor, minus reference, sum
+        float2 hf[NT <= 2 ? NT : 1], nm[NT], l[NT];  // rows 8 j + 2 tig, + 1: score factor, minus reference, sum
+        uint32_t fresh = (1u << (2 * NT)) - 1u;  // rows without a reference yet (nm 0): bits 2 j, 2 j + 1
         float acc[DT][NT][4];
         float vcur = 0.f, vinv = 0.f, vmax = 0.f;  // the accumulators' unit, 1 over it, the largest v_scale so far
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            hf[j] = *reinterpret_cast<const float2*>(hfac + 8 * j + 2 * tig);
-            nm[j] = make_float2(INFINITY, INFINITY);
+            if (NT <= 2) hf[j] = *reinterpret_cast<const float2*>(hfac + 8 * j + 2 * tig);
+            nm[j] = make_float2(0.f, 0.f);
             l[j] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt)
@@ -479,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
             for (int h0 = 0; h0 < P; h0 += HJ) {
                 int pos0[HJ];
-                float ks[HJ], vs[HJ], sc[HJ][NT][4], x[HJ][NT][4];
+                float ks[HJ], vs[HJ], x[HJ][NT][4];
                 bool masked = false;  // a limit per row matters
 #pragma unroll
                 for (int z = 0; z < HJ; ++z) {
@@ -488,10 +517,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                     ks[z] = ti.ks;
                     vs[z] = ti.vs;
                     masked = masked || ti.pos0 + 16 > lim0;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) sc[z][j][k] = 0.f;
                 }
                 const uint32_t stage = ring_at + (uint32_t)at * kStageBytes + h0 * 2 * S::kTile;
                 // scores of 16 positions (rows) and the unit's query rows (columns)
@@ -515,8 +540,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
                             for (int j = 0; j < NT; ++j) {
                                 const uint4 q4 = NT == 1 ? qf[2 * h + t] : *reinterpret_cast<const uint4*>(qh + (8 * j + gid) * QP + 64 * h + 16 * tig + 8 * t);
-                                mma_f16_16816(sc[z][j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
-                                mma_f16_16816(sc[z][j], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
+                                if (h == 0 && t == 0) mma_f16_first(x[z][j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
+                                else mma_f16_16816(x[z][j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
+                                mma_f16_16816(x[z][j], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
                             }
                         }
                     }
@@ -526,9 +552,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 for (int z = 0; z < HJ; ++z)
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        const float2 f = mul2(hf[j], make_float2(ks[z], ks[z]));
-                        const float2 x0 = fma2(make_float2(sc[z][j][0], sc[z][j][1]), f, nm[j]);
-                        const float2 x1 = fma2(make_float2(sc[z][j][2], sc[z][j][3]), f, nm[j]);
+                        const float2 hfj = NT <= 2 ? hf[NT <= 2 ? j : 0] : *reinterpret_cast<const float2*>(hfac + 8 * j + 2 * tig);
+                        const float2 f = mul2(hfj, make_float2(ks[z], ks[z]));
+                        const float2 x0 = fma2(make_float2(x[z][j][0], x[z][j][1]), f, nm[j]);
+                        const float2 x1 = fma2(make_float2(x[z][j][2], x[z][j][3]), f, nm[j]);
                         x[z][j][0] = x0.x, x[z][j][1] = x0.y, x[z][j][2] = x1.x, x[z][j][3] = x1.y;
                     }
                 if (masked)
@@ -548,30 +575,26 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
                         top = fmaxf(top, fmaxf(fmaxf(x[z][j][0], x[z][j][1]), fmaxf(x[z][j][2], x[z][j][3])));
-                if (__any_sync(0xffffffffu, top > kRaise)) {  // a new reference for every row
+                if (__any_sync(0xffffffffu, top > kRaise || fresh)) {
+                    // the references move by d: up to the largest score, or to a row's first one
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        float nmj[2] = {nm[j].x, nm[j].y}, al[2];
-                        const float hfj[2] = {hf[j].x, hf[j].y};
+                        float d[2], al[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float m = -INFINITY;
 #pragma unroll
-                            for (int z = 0; z < HJ; ++z) {
-                                const float f = hfj[e] * ks[z];
-                                if (x[z][j][e] != -INFINITY) m = fmaxf(m, sc[z][j][e] * f);
-                                if (x[z][j][2 + e] != -INFINITY) m = fmaxf(m, sc[z][j][2 + e] * f);
-                            }
+                            for (int z = 0; z < HJ; ++z) m = fmaxf(m, fmaxf(x[z][j][e], x[z][j][2 + e]));
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            const float mn = fmaxf(-nmj[e], m);
-                            al[e] = nmj[e] == INFINITY ? 0.f : ex2(-nmj[e] - mn);
-                            nmj[e] = -mn;
+                            const bool isnew = (fresh >> (2 * j + e)) & 1u;
+                            d[e] = isnew ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
+                            al[e] = isnew ? 0.f : ex2(-d[e]);
+                            if (isnew && m != -INFINITY) fresh &= ~(1u << (2 * j + e));
 #pragma unroll
                             for (int z = 0; z < HJ; ++z) {
-                                const float f = hfj[e] * ks[z];
-                                if (x[z][j][e] != -INFINITY) x[z][j][e] = fmaf(sc[z][j][e], f, -mn);
-                                if (x[z][j][2 + e] != -INFINITY) x[z][j][2 + e] = fmaf(sc[z][j][2 + e], f, -mn);
+                                x[z][j][e] -= d[e];
+                                x[z][j][2 + e] -= d[e];
                             }
 #pragma unroll
                             for (int dt = 0; dt < DT; ++dt) {
@@ -579,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                                 acc[dt][j][2 + e] *= al[e];
                             }
                         }
-                        nm[j] = make_float2(nmj[0], nmj[1]);
+                        nm[j] = make_float2(nm[j].x - d[0], nm[j].y - d[1]);
                         l[j] = mul2(l[j], make_float2(al[0], al[1]));
                     }
                 }
@@ -741,7 +764,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         float mr[NT][2], ls[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            mr[j][0] = -nm[j].x, mr[j][1] = -nm[j].y;
+            mr[j][0] = (fresh >> (2 * j)) & 1u ? -INFINITY : -nm[j].x;
+            mr[j][1] = (fresh >> (2 * j + 1)) & 1u ? -INFINITY : -nm[j].y;
             ls[j][0] = l[j].x, ls[j][1] = l[j].y;
         }
 #pragma unroll
@@ -852,7 +876,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 }
         }
         first = false;
-    } while (next_unit(pl));
+        if (!next_unit(pl)) break;
+        load_q();
+    } while (true);
     // after a timeout: wait (again with a limit) for the copies that are still in flight
     if (*abort && lane == 0)
         for (int s = 0; s < ST; ++s) mbar_wait_bounded(&full[warp * ST + s], ph ^ (s < st ? 1u : 0u), nullptr, kWaitLimitCycles / 8);
@@ -1007,15 +1033,11 @@ __global__ void __launch_bounds__(256) block_mass_kernel(const __grid_constant__
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // Query rows per unit, as 8 NT: a head's rows in as few row tiles as the accumulators allow
-// (64 rows of 64 dims, 32 of 128, 16 of 256: 128 registers), of the smallest NT that is built
-// and holds an equal share of them. (40 rows of 64 dims: one tile of NT 5 reads every code once;
-// two tiles of NT 4 took 100 us where it takes a third of that.)
+// (40 rows of 64 dims, 32 of 128, 16 of 256), each with an equal share of them.
 int pick_nt(int hd, int64_t rows) {
-    const int most = hd == 64 ? 8 : hd == 128 ? 4 : 2;
+    const int most = hd == 64 ? 5 : hd == 128 ? 4 : 2;
     const int64_t tiles = (rows + 8 * most - 1) / (8 * most);
-    const int need = (int)((rows + 8 * tiles - 1) / (8 * tiles));
-    if (hd == 64 && need > 3) return need <= 5 ? 5 : 8;
-    return need;
+    return (int)((rows + 8 * tiles - 1) / (8 * tiles));
 }
 
 struct Layout {
@@ -1105,15 +1127,12 @@ cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& km, const CUtens
 template <int HD, bool SPARSE>
 cudaError_t launch_attn_nt(int nt, const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
     if (nt == 1) return launch_attn<HD, 1, SPARSE>(p, km, vm, sms, s);
-    if constexpr (!SPARSE && HD == 64) {
-        if (nt == 3) return launch_attn<HD, 3, SPARSE>(p, km, vm, sms, s);
-        if (nt == 5) return launch_attn<HD, 5, SPARSE>(p, km, vm, sms, s);
-        if (nt == 8) return launch_attn<HD, 8, SPARSE>(p, km, vm, sms, s);
-    }
-    if constexpr (!SPARSE && HD == 128) {
+    if constexpr (!SPARSE && HD <= 128) {
         if (nt == 3) return launch_attn<HD, 3, SPARSE>(p, km, vm, sms, s);
         if (nt == 4) return launch_attn<HD, 4, SPARSE>(p, km, vm, sms, s);
     }
+    if constexpr (!SPARSE && HD == 64)
+        if (nt == 5) return launch_attn<HD, 5, SPARSE>(p, km, vm, sms, s);
     return launch_attn<HD, 2, SPARSE>(p, km, vm, sms, s);
 }
 
