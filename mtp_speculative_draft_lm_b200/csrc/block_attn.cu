@@ -100,7 +100,7 @@ struct Shape {
     static constexpr int P = HD == 256 ? 1 : 2;                  // tiles per step
     // of them worked on together, and CTAs per SM: as the accumulators leave registers
     static constexpr int kJoint = HD < 256 && NT <= 2 ? P : 1;
-    static constexpr int kPerSm = HD == 64 ? (NT <= 2 ? 3 : 2) : HD == 128 ? (NT <= 1 ? 3 : 2) : 2;
+    static constexpr int kPerSm = HD == 64 ? (NT <= 3 ? 3 : 2) : HD == 128 ? (NT <= 1 ? 3 : 2) : 2;
     static constexpr int kQPitch = HD + 8;                       // f16 elements
     static constexpr int kRows = 8 * NT;
     static constexpr size_t kFixed = (size_t)HD * NT * 64           // two warps' accumulators
@@ -1090,23 +1090,6 @@ bool cache_map(CUtensorMap* m, const BlockCache& c, const uint8_t* base) {
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, c.hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Launches `kern` so that it may start while the kernel before it in the stream ends (each of
-// ours waits for that before it touches memory).
-template <class K, class... A>
-cudaError_t launch_after(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int HD, int NT, bool SPARSE>

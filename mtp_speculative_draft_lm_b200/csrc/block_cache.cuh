@@ -145,4 +145,21 @@ __device__ void pick_in_order(const Key& key, int n, uint32_t thr, int need, Pic
     }
 }
 
+// Launches `kern` so that it may start while the kernel before it in the stream ends (each of
+// ours waits for that before it touches memory).
+template <class K, class... A>
+cudaError_t launch_after(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace mtp
