@@ -67,8 +67,19 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
     return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
-// Grid (K or V of each head, groups of touched blocks, sequences).
-template <int HD, int BS>
+// sum[0 .. 8) += the values of 8 codes.
+__device__ __forceinline__ void add_codes(float (&sum)[8], const uint2& o) {
+    const uint32_t w[2] = {o.x, o.y};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        add_halves(sum[2 * u], sum[2 * u + 1], e4m3x2_to_f16x2((uint16_t)(w[u >> 1] >> (16 * (u & 1)))));
+}
+
+// Grid (K or V of each head, groups of touched blocks, sequences). OLD: the earlier rows' codes of
+// a block that already has some are asked for together with the new rows (a step's latency
+// counts: nearly all of its blocks have some), else only once they are needed (a prompt has one
+// such block, and the registers hold more rows in flight instead).
+template <int HD, int BS, bool OLD>
 __global__ void __launch_bounds__(kAppThreads) block_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int WPJ = BS / 16;                // warps per block
     constexpr int JPC = kAppThreads / 32 / WPJ;  // blocks per CTA at a time
@@ -107,24 +118,30 @@ __global__ void __launch_bounds__(kAppThreads) block_append_kernel(const __grid_
         float* scale_at = (is_v ? p.c.v_scale : p.c.k_scale) + (int64_t)max(phys, 0) * p.c.nkv + g;
 
         uint4 in[NI];
-        uint2 was[NI];
+        uint2 was[OLD ? NI : 1];
         float s_old = 0.f;
         uint32_t am = 0;
+        // this lane's rows are pos0 + sub + RPI i: new ones for i in [i0, i1)
+        const int i0 = beg > pos0 + sub ? min((beg - pos0 - sub + RPI - 1) / RPI, NI) : 0;
+        const int i1 = s.len > pos0 + sub ? min((s.len - pos0 - sub + RPI - 1) / RPI, NI) : 0;
+        const int64_t code_step = RPI * p.c.row_stride;
         if (work) {
+            const uint16_t* row = x + (int64_t)(pos0 + sub - beg) * p.kv_stride;
+            const int64_t step = RPI * p.kv_stride;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int pos = pos0 + i * RPI + sub;
                 in[i] = make_uint4(0, 0, 0, 0);
-                if (pos >= beg && pos < s.len) in[i] = ldg_stream(x + (int64_t)(pos - beg) * p.kv_stride);
+                if (i >= i0 && i < i1) in[i] = ldg_stream(row);
+                row += step;
             }
             if (has_old) {
                 s_old = *scale_at;
+                if (OLD)
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    was[i] = make_uint2(0, 0);
-                    if (pos0 + i * RPI + sub < beg)
-                        was[i] = *reinterpret_cast<const uint2*>(codes + (int64_t)(i * RPI) * p.c.row_stride);
-                }
+                    for (int i = 0; i < NI; ++i) {
+                        was[OLD ? i : 0] = make_uint2(0, 0);
+                        if (i < i0) was[OLD ? i : 0] = *reinterpret_cast<const uint2*>(codes + i * code_step);
+                    }
             }
 #pragma unroll
             for (int i = 0; i < NI; ++i) am = max_bits2(max_bits2(max_bits2(max_bits2(am, in[i].x), in[i].y), in[i].z), in[i].w);
@@ -152,42 +169,50 @@ __global__ void __launch_bounds__(kAppThreads) block_append_kernel(const __grid_
             // a power of two's reciprocal is exact, and so is the product's rounding the quotient's
             const bool pow2 = (__float_as_uint(sc) & 0x7fffffu) == 0 && sc >= 1.17549435e-38f && sc <= 8.5e37f;
             const float by = sc > 0.f ? sc : 1.f;  // (x itself where everything is zero or not finite)
-            const float inv = __fdiv_rn(1.f, by);
-            const bool grow = has_old && sc != s_old;
-            const float ratio = grow ? __fdiv_rn(s_old, sc) : 1.f;
+            if ((pow2 || sc == 0.f) && !has_old) {
+                // (rows behind the sequence are zeros, and count as such in the mean)
+                const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(sc)) : 1.f;
+                uint8_t* out = codes;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int pos = pos0 + i * RPI + sub;
-                const bool isnew = pos >= beg && pos < s.len, isold = has_old && pos < beg;
-                uint2 o = make_uint2(0, 0);
-                if (pow2 || sc == 0.f) {
-                    o = encode8(in[i], inv);
-                } else {  // a scale that an append did not write
-                    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-                    uint32_t q[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) q[u] = f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(w[u]), by), __fdiv_rn(bf16_hi(w[u]), by));
-                    o = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                for (int i = 0; i < NI; ++i) {
+                    const uint2 o = encode8(in[i], inv);
+                    if (i < i1) *reinterpret_cast<uint2*>(out) = o;
+                    out += code_step;
+                    if (mean) add_codes(sum, o);
                 }
-                if (has_old && isold) {
-                    o = was[i];
-                    if (grow) {
-                        const uint32_t w[2] = {o.x, o.y};
-                        uint32_t q[4];
+            } else {
+                const bool grow = has_old && sc != s_old;
+                const float ratio = grow ? __fdiv_rn(s_old, sc) : 1.f;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[u >> 1] >> (16 * (u & 1)))));
-                            q[u] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+                for (int i = 0; i < NI; ++i) {
+                    uint2 o = make_uint2(0, 0);
+                    uint8_t* out = codes + i * code_step;
+                    if (i < i0) {
+                        o = OLD ? was[OLD ? i : 0] : *reinterpret_cast<const uint2*>(out);
+                        if (grow) {
+                            const uint32_t w[2] = {o.x, o.y};
+                            uint32_t q[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[u >> 1] >> (16 * (u & 1)))));
+                                q[u] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+                            }
+                            o = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                            *reinterpret_cast<uint2*>(out) = o;
                         }
-                        o = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-                    }
-                }
-                if (isnew || (isold && grow)) *reinterpret_cast<uint2*>(codes + (int64_t)(i * RPI) * p.c.row_stride) = o;
-                if (mean) {  // (rows behind the sequence are zeros here)
-                    const uint32_t w[2] = {o.x, o.y};
+                    } else if (i < i1) {
+                        if (pow2) {
+                            o = encode8(in[i], __uint_as_float((254u << 23) - __float_as_uint(sc)));
+                        } else {  // a scale that an append did not write
+                            const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+                            uint32_t q[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        add_halves(sum[2 * u], sum[2 * u + 1], e4m3x2_to_f16x2((uint16_t)(w[u >> 1] >> (16 * (u & 1)))));
+                            for (int u = 0; u < 4; ++u) q[u] = f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(w[u]), by), __fdiv_rn(bf16_hi(w[u]), by));
+                            o = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                        }
+                        *reinterpret_cast<uint2*>(out) = o;
+                    }
+                    if (mean) add_codes(sum, o);
                 }
             }
         }
@@ -246,9 +271,13 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
     const int jpc = kAppThreads / 32 / (p.c.bs / 16);
     const int groups = (p.touch + jpc - 1) / jpc;
     const dim3 grid((unsigned)(2 * p.c.nkv), (unsigned)(groups < 65535 ? groups : 65535), (unsigned)p.t.B);
-    if (p.c.bs == 16) return launch_after(block_append_kernel<HD, 16>, grid, kAppThreads, 0, s, p);
-    if (p.c.bs == 32) return launch_after(block_append_kernel<HD, 32>, grid, kAppThreads, 0, s, p);
-    return launch_after(block_append_kernel<HD, 64>, grid, kAppThreads, 0, s, p);
+    // (a 16-token step was as fast either way)
+    if (p.t.T <= 16) return p.c.bs == 16 ? launch_after(block_append_kernel<HD, 16, true>, grid, kAppThreads, 0, s, p)
+                          : p.c.bs == 32 ? launch_after(block_append_kernel<HD, 32, true>, grid, kAppThreads, 0, s, p)
+                                         : launch_after(block_append_kernel<HD, 64, true>, grid, kAppThreads, 0, s, p);
+    return p.c.bs == 16 ? launch_after(block_append_kernel<HD, 16, false>, grid, kAppThreads, 0, s, p)
+         : p.c.bs == 32 ? launch_after(block_append_kernel<HD, 32, false>, grid, kAppThreads, 0, s, p)
+                        : launch_after(block_append_kernel<HD, 64, false>, grid, kAppThreads, 0, s, p);
 }
 
 }  // namespace
