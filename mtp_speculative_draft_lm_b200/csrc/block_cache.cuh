@@ -44,104 +44,129 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // 1 / 127 rounded to fp32: the step of 8-bit integers is the largest magnitude times this.
 constexpr float kInv127 = 1.f / 127.f;
 
-constexpr int kPickThreads = 1024;
-
+// The `want` smallest of a list of keys in (key, index) order, by one CTA of THREADS threads that
+// hold KEYS keys each, key u of thread t being entry u THREADS + t (whole rows of loads and
+// stores). Digits are counted from the top among the keys that share the digits found so far
+// until a count ends exactly at `want`: of 8 bits for 256 threads, of 11 for 1,024 (2.7 and 3.4
+// thousand cycles for 512 and 2,048 spread floats, 6.3 for 8,192; most of it barriers). Integer
+// counts: the choice is exact.
+template <int THREADS>
 struct PickSmem {
-    uint32_t hist[256];
+    static constexpr int kBits = THREADS <= 256 ? 8 : 11, kBins = 1 << kBits, kWarps = THREADS / 32;
+    uint32_t hist[kBins];
+    uint32_t tot[kWarps * 8];  // taken in each warp's row of 32 entries, then before it
     uint32_t warp_sum[32];
-    uint32_t digit, before;
+    uint32_t digit, before, in_digit;
 };
 
-// The `want` (1 <= want <= n) smallest of key(0) .. key(n - 1) in (key, index) order: every
-// key < thr, and the first `need` of those equal to thr. Four passes over 8-bit digits from
-// the top, each a histogram of the keys that share the digits found so far. All of the
-// block's kPickThreads threads call it; integer counts, so the result is exact.
-template <class Key>
-__device__ void pick_threshold(const Key& key, int n, int want, PickSmem& sm, uint32_t* thr, int* need) {
+__device__ __forceinline__ uint32_t warp_inclusive(uint32_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)(threadIdx.x & 31) >= o) v += u;
+    }
+    return v;
+}
+
+// Keys below *thr are picked, and the first *need of those equal to it (1 <= want <= the number
+// of keys). each(f) calls f(key) for every key that this thread holds.
+template <int THREADS, class Each>
+__device__ __forceinline__ void pick_threshold(const Each& each, uint32_t want, PickSmem<THREADS>& sm, uint32_t* thr, uint32_t* need) {
+    using S = PickSmem<THREADS>;
+    constexpr int PER = S::kBins / THREADS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t prefix = 0, mask = 0;
-    const int tid = threadIdx.x;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) sm.hist[tid] = 0;
+#pragma unroll 1
+    for (int shift = 32 - S::kBits;;) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sm.hist[j * THREADS + tid] = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kPickThreads) {
-            const uint32_t k = key(i);
-            if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & 255u], 1u);
-        }
+        each([&](uint32_t k) {
+            if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & (S::kBins - 1)], 1u);
+        });
         __syncthreads();
-        if (tid < 32) {  // the first digit at which the running count reaches `want`
-            uint32_t c[8], sum = 0;
+        // the warp, then the lane, then the counter at which the running count reaches `want`
+        uint32_t c[PER], sum = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += c[j] = sm.hist[8 * tid + j];
-            uint32_t inc = sum;
+        for (int j = 0; j < PER; ++j) sum += c[j] = sm.hist[PER * tid + j];
+        const uint32_t wsum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) sm.warp_sum[warp] = wsum;
+        __syncthreads();
+        const uint32_t w = lane < S::kWarps ? sm.warp_sum[lane] : 0u, winc = warp_inclusive(w);
+        const int src = __ffs(__ballot_sync(0xffffffffu, winc >= want)) - 1;
+        uint32_t run = __shfl_sync(0xffffffffu, winc - w, src);
+        if (warp == src) {
+            const uint32_t inc = run + warp_inclusive(sum);
+            if (lane == __ffs(__ballot_sync(0xffffffffu, inc >= want)) - 1) {
+                run = inc - sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-                if (tid >= o) inc += u;
-            }
-            uint32_t run = inc - sum;  // keys in the digits before this lane's
-            const bool here = run < (uint32_t)want && inc >= (uint32_t)want;
-            if (here) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (run < (uint32_t)want && run + c[j] >= (uint32_t)want) {
-                        sm.digit = 8 * tid + j;
+                for (int j = 0; j < PER; ++j) {
+                    if (run < want && run + c[j] >= want) {
+                        sm.digit = PER * tid + j;
                         sm.before = run;
+                        sm.in_digit = c[j];
                     }
                     run += c[j];
                 }
             }
         }
         __syncthreads();
-        prefix |= sm.digit << shift;
-        mask |= 255u << shift;
-        want -= (int)sm.before;
+        const uint32_t digit = sm.digit;
+        prefix |= digit << shift;
+        mask |= (uint32_t)(S::kBins - 1) << shift;
+        want -= sm.before;
+        const uint32_t next = prefix + (1u << shift);
+        if (shift && sm.in_digit == want && next) {  // all of this digit's keys
+            *thr = next;
+            *need = 0;
+            return;
+        }
+        if (shift == 0) break;
+        // (the last digit may overlap the one before: those bits are the prefix's already)
+        shift = shift >= S::kBits ? shift - S::kBits : 0;
     }
     *thr = prefix;
     *need = want;
 }
 
-// Exclusive prefix sum of v (its sum over the block below 2^32) over the block's threads;
-// *total gets the sum.
-__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, PickSmem& sm, uint32_t* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t inc = v;
+// Where each key stands: *taken bit u says whether key u is picked, before[u] how many picked
+// ones come before it in index order. All threads call it; a block barrier lies between the last
+// read of k and the return.
+template <int THREADS, int KEYS>
+__device__ __forceinline__ void pick_places(const uint32_t (&k)[KEYS], int n, uint32_t thr, uint32_t need, PickSmem<THREADS>& sm,
+                                            uint32_t* taken, uint32_t (&before)[KEYS]) {
+    static_assert(KEYS <= 8, "sm.tot");
+    constexpr int W = THREADS / 32, N = KEYS * W;  // rows of 32 entries, in index order
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
+    for (int u = 0; u < KEYS; ++u) {
+        const bool in = u * THREADS + tid < n;
+        const uint32_t lt = __ballot_sync(0xffffffffu, in && k[u] < thr), eq = __ballot_sync(0xffffffffu, in && k[u] == thr);
+        before[u] = (uint32_t)__popc(lt & below) | (uint32_t)__popc(eq & below) << 16;  // in the row
+        if (lane == 0) sm.tot[u * W + warp] = (uint32_t)__popc(lt) | (uint32_t)__popc(eq) << 16;
     }
-    __syncthreads();  // the previous use of warp_sum is over
-    if (lane == 31) sm.warp_sum[warp] = inc;
     __syncthreads();
-    uint32_t w = sm.warp_sum[lane], winc = w;
+    if (warp == 0) {
+        constexpr int PER = (N + 31) / 32;
+        uint32_t c[PER], sum = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, winc, o);
-        if (lane >= o) winc += u;
+        for (int j = 0; j < PER; ++j) sum += c[j] = PER * lane + j < N ? sm.tot[PER * lane + j] : 0u;
+        uint32_t run = warp_inclusive(sum) - sum;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (PER * lane + j < N) sm.tot[PER * lane + j] = run;
+            run += c[j];
+        }
     }
-    *total = __shfl_sync(0xffffffffu, winc, 31);
-    return inc - v + (warp ? __shfl_sync(0xffffffffu, winc, warp - 1) : 0u);
-}
-
-// Calls emit(i, taken, before) for every i < n in chunks of the block's threads, in order of
-// i: whether i is among the picked, and how many picked ones come before it. Between a
-// chunk's read(i) and its emit there is a block barrier, so emit may overwrite places that
-// this or earlier chunks' reads used. read returns what emit gets as its last argument.
-template <class Key, class Read, class Emit>
-__device__ void pick_in_order(const Key& key, int n, uint32_t thr, int need, PickSmem& sm, const Read& read,
-                              const Emit& emit) {
-    uint32_t below = 0, equal = 0;  // picked for sure, and equal to thr, before this chunk
-    for (int base = 0; base < n; base += kPickThreads) {
-        const int i = base + (int)threadIdx.x;
-        const uint32_t k = i < n ? key(i) : 0xffffffffu;
-        const bool lt = i < n && k < thr, eq = i < n && k == thr;
-        const auto val = read(i < n ? i : n - 1);
-        uint32_t total;
-        const uint32_t at = block_exclusive((lt ? 1u : 0u) | (eq ? 0x10000u : 0u), sm, &total);
-        const uint32_t b_lt = below + (at & 0xffffu), b_eq = equal + (at >> 16);
-        if (i < n) emit(i, lt || (eq && b_eq < (uint32_t)need), b_lt + min(b_eq, (uint32_t)need), val);
-        below += total & 0xffffu;
-        equal += total >> 16;
+    __syncthreads();
+    *taken = 0;
+#pragma unroll
+    for (int u = 0; u < KEYS; ++u) {
+        const uint32_t at = before[u] + sm.tot[u * W + warp], eq = at >> 16;
+        const bool in = u * THREADS + tid < n;
+        if (in && (k[u] < thr || (k[u] == thr && eq < need))) *taken |= 1u << u;
+        before[u] = (at & 0xffffu) + min(eq, need);
     }
 }
 

@@ -2,14 +2,16 @@
 //
 // Selection: a block's score for a token and kv head is the largest, over the group's query
 // heads, of an 8-bit dot product with the block's mean key. The dot is a whole number (127 127
-// 256 < 2^24) and each fp32 step is rounded to nearest, so the scores, and with them the chosen
-// blocks, are the same bits everywhere; ties go to the lowest index. The scores are bound by
-// reading the means (hd + 4 bytes per block and head); the choice is four histogram passes
-// over the scores by one CTA for each token and head, then one ordered pass that writes the
-// list ascending.
+// 256 < 2^24, as fp32 exact) and each fp32 step is rounded to nearest, so the scores, and with
+// them the chosen blocks, are the same bits everywhere; ties go to the lowest index. The
+// scores are bound by reading the means (hd + 4 bytes per block and head): a warp takes 16
+// blocks of a head at a time, whose bytes are the A operand of mma.sync m16n8k32 as they come
+// (a lane's 16-byte loads, the K dimension permuted alike in q), for all of the step's tokens.
+// The choice is one CTA for each token and head, its keys in registers: a search for the last
+// chosen key, then one prefix sum that gives every chosen block its place in the ascending list.
 //
-// Eviction: the same choice of the smallest accumulated weights by one CTA per sequence, and
-// one ordered pass that moves the table and the weights up in place.
+// Eviction: the same choice of the smallest accumulated weights by one CTA per sequence, whose
+// prefix sum moves the table and the weights up, in place where asked.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -21,7 +23,18 @@ namespace mtp {
 namespace {
 
 constexpr int kScThreads = 256;
-constexpr int kMaxGroup = 16;
+constexpr int kScRows = 128;  // query rows in 8 bits (padded groups) at a time
+
+// Sum over the block's threads, in every one of them.
+template <int THREADS>
+__device__ __forceinline__ int block_sum(int v, PickSmem<THREADS>& sm) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sm.warp_sum[threadIdx.x >> 5] = (uint32_t)v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    return __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? (int)sm.warp_sum[lane] : 0);
+}
 
 struct SelectParams {
     BlockCache c;
@@ -31,114 +44,211 @@ struct SelectParams {
     int group;
     int n_sel, n_first, n_last;
     int32_t* sel;
-    float* score;  // [B, T, nkv, n_table]
+    uint32_t* keys;  // [B, T, nkv, n_table]: the score's order, smallest best
 };
 
-// Grid (rows = B T nkv, chunks of kScThreads blocks): one block's score per thread.
+// D[16 x 8] += A[16 x 32] B[32 x 8], 8-bit integers.
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Bytes between the 8-bit query rows in shared memory: two rows' 64-byte pieces in other banks.
+template <int HD>
+__host__ __device__ constexpr int q8_pitch() { return HD == 64 ? 64 : HD + 64; }
+// Rows a token takes there: its group, padded to the matrix unit's 8 columns.
+__host__ __device__ inline int group_rows(int group) { return (group + 7) & ~7; }
+
+// Grid (parts of the blocks, kv heads, sequences). The query rows are quantized to shared
+// memory up to kScRows at a time; a warp has the next tile's blocks looked up while it waits for
+// this tile's means.
 template <int HD>
 __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_constant__ SelectParams p) {
-    __shared__ __align__(16) int8_t q8[kMaxGroup][HD];
-    __shared__ float sq[kMaxGroup];
-    const int64_t row = blockIdx.x;
-    const int g = (int)(row % p.c.nkv);
-    const int64_t bt = row / p.c.nkv;
-    const int b = (int)(bt / p.t.T), tok = (int)(bt % p.t.T);
+    constexpr int C = HD / 64;  // 16-byte chunks of a lane, 64 bytes apart
+    __shared__ __align__(16) uint8_t q8[kScRows * q8_pitch<HD>()];
+    __shared__ float sq[kScRows];
+    const int g = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
     const SeqStep s = seq_step(p.t, b);
-    if (tok >= s.q) return;
-    const int nb = blocks_of(s.len - s.q + tok + 1, p.c.bs, p.t.n_table);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int j0 = blockIdx.y * kScThreads; j0 < nb; j0 += gridDim.y * kScThreads) {
-        if (j0 == (int)(blockIdx.y * kScThreads)) {
-            for (int h = warp; h < p.group; h += kScThreads / 32) {
-                const uint16_t* src = p.q + bt * p.q_stride + ((int64_t)g * p.group + h) * HD;
-                float v[HD / 32], mx = 0.f;
-                bool odd = false;  // an infinity or NaN
+    const int nb = blocks_of(s.len, p.c.bs, p.t.n_table);
+    if (s.q == 0 || (int)blockIdx.x * (kScThreads / 2) >= nb) return;
+    const int gr = group_rows(p.group), chunk = kScRows / gr;  // tokens at a time
+    const int gid = lane >> 2, tig = lane & 3;
+    const int j_first = ((int)blockIdx.x * (kScThreads / 32) + warp) * 16, j_step = (int)gridDim.x * (kScThreads / 2);
+    // blocks j + gid and j + gid + 8
+    auto look_up = [&](int j, int (&n)[2]) {
 #pragma unroll
-                for (int i = 0; i < HD / 32; ++i) {
-                    v[i] = bf16_to_f32(src[lane + 32 * i]);
-                    mx = fmaxf(mx, fabsf(v[i]));
-                    odd = odd || !(fabsf(v[i]) < INFINITY);
-                }
-#pragma unroll
-                for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                odd = __any_sync(0xffffffffu, odd);
-                const float sc = __fmul_rn(mx, kInv127);
-#pragma unroll
-                for (int i = 0; i < HD / 32; ++i)
-                    q8[h][lane + 32 * i] = odd || sc == 0.f ? 0 : (int8_t)__float2int_rn(__fdiv_rn(v[i], sc));
-                if (lane == 0) sq[h] = odd ? -1.f : sc;
-            }
-            __syncthreads();
-        }
-        const int j = j0 + threadIdx.x;
-        if (j < nb) {
-            const int phys = table_block(p.t, p.c.num_blocks, b, j);
-            float best = -INFINITY;
-            if (phys >= 0) {
-                const int64_t at = (int64_t)phys * p.c.nkv + g;
-                const int4* m = reinterpret_cast<const int4*>(p.c.k_mean + at * HD);
-                const float sk = p.c.k_mean_scale[at];
-                int dot[kMaxGroup];
-#pragma unroll
-                for (int h = 0; h < kMaxGroup; ++h) dot[h] = 0;
-                for (int i = 0; i < HD / 16; ++i) {
-                    const int4 mv = m[i];
-#pragma unroll
-                    for (int h = 0; h < kMaxGroup; ++h)
-                        if (h < p.group) {
-                            const int4 qv = *reinterpret_cast<const int4*>(&q8[h][16 * i]);
-                            dot[h] = __dp4a(mv.x, qv.x, dot[h]);
-                            dot[h] = __dp4a(mv.y, qv.y, dot[h]);
-                            dot[h] = __dp4a(mv.z, qv.z, dot[h]);
-                            dot[h] = __dp4a(mv.w, qv.w, dot[h]);
-                        }
-                }
-                bool nan = false;
-#pragma unroll
-                for (int h = 0; h < kMaxGroup; ++h)
-                    if (h < p.group && sq[h] >= 0.f) {
-                        const float f = __fmul_rn((float)dot[h], __fmul_rn(sq[h], sk));
-                        nan = nan || f != f;
-                        best = fmaxf(best, f);
-                    }
-                if (nan) best = __uint_as_float(0x7fc00000u);
+        for (int h = 0; h < 2; ++h) n[h] = j + gid + 8 * h < nb ? table_block(p.t, p.c.num_blocks, b, j + gid + 8 * h) : -1;
+    };
+    for (int t0 = 0; t0 < s.q; t0 += chunk) {
+    const int t1 = min(s.q, t0 + chunk), rows = (t1 - t0) * gr;
+    int next[2];
+    look_up(j_first, next);
+    if (t0) __syncthreads();  // the earlier rows have been used
+    for (int r = warp; r < rows; r += kScThreads / 32) {
+        const int tok = t0 + r / gr, i = r % gr;
+        const bool has = i < p.group;
+        float v[HD / 32], mx = 0.f;
+        bool odd = !has;  // no head, or one with an infinity or NaN
+        if (has) {
+            const uint16_t* src = p.q + ((int64_t)b * p.t.T + tok) * p.q_stride + ((int64_t)g * p.group + i) * HD + lane * (HD / 32);
+            if constexpr (HD == 64) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(src);
+                v[0] = bf16_lo(w), v[1] = bf16_hi(w);
             } else {
-                raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
+#pragma unroll
+                for (int u = 0; u < HD / 128; ++u) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(src + 4 * u);
+                    v[4 * u] = bf16_lo(w.x), v[4 * u + 1] = bf16_hi(w.x), v[4 * u + 2] = bf16_lo(w.y), v[4 * u + 3] = bf16_hi(w.y);
+                }
             }
-            p.score[row * p.t.n_table + j] = best;
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k) {
+                mx = fmaxf(mx, fabsf(v[k]));
+                odd = odd || !(fabsf(v[k]) < INFINITY);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k) v[k] = 0.f;
         }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        odd = __any_sync(0xffffffffu, odd);
+        const float sc = __fmul_rn(mx, kInv127);
+        uint32_t w[(HD / 32 + 3) / 4] = {};
+        if (!odd && sc > 0.f)
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k)
+                w[k >> 2] |= ((uint32_t)__float2int_rn(__fdiv_rn(v[k], sc)) & 255u) << (8 * (k & 3));
+        uint8_t* dst = q8 + r * q8_pitch<HD>() + lane * (HD / 32);
+        if constexpr (HD == 64) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
+        else
+#pragma unroll
+            for (int u = 0; u < HD / 128; ++u) reinterpret_cast<uint32_t*>(dst)[u] = w[u];
+        if (lane == 0) sq[r] = odd ? -1.f : sc;
+    }
+    __syncthreads();
+    for (int j0 = j_first; j0 < nb; j0 += j_step) {
+        // rows gid and gid + 8 of the tile: blocks j0 + gid and 8 on
+        uint4 m[2][C];
+        float sk[2];
+        bool has[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = j0 + gid + 8 * h;
+            const int n = next[h];
+            has[h] = n >= 0;
+            if (j < nb && n < 0 && tig == 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
+            sk[h] = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) m[h][c] = make_uint4(0, 0, 0, 0);
+            if (has[h]) {
+                const int64_t at = (int64_t)n * p.c.nkv + g;
+                sk[h] = p.c.k_mean_scale[at];
+#pragma unroll
+                for (int c = 0; c < C; ++c) m[h][c] = *reinterpret_cast<const uint4*>(p.c.k_mean + at * HD + 64 * c + 16 * tig);
+            }
+        }
+        look_up(j0 + j_step, next);
+        for (int tok = t0; tok < t1; ++tok) {
+            float best[2] = {-INFINITY, -INFINITY};
+            bool nan[2] = {false, false};
+            for (int r0 = (tok - t0) * gr; r0 < (tok - t0 + 1) * gr; r0 += 8) {
+                int d[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(q8 + (r0 + gid) * q8_pitch<HD>() + 64 * c + 16 * tig);
+                    mma_s8(d, m[0][c].x, m[1][c].x, m[0][c].y, m[1][c].y, q.x, q.y);
+                    mma_s8(d, m[0][c].z, m[1][c].z, m[0][c].w, m[1][c].w, q.z, q.w);
+                }
+                const float2 sc = *reinterpret_cast<const float2*>(sq + r0 + 2 * tig);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = __fmul_rn((float)d[2 * h + e], __fmul_rn(e ? sc.y : sc.x, sk[h]));
+                        if ((e ? sc.y : sc.x) >= 0.f) {
+                            nan[h] = nan[h] || f != f;
+                            best[h] = fmaxf(best[h], f);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 1));
+                best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 2));
+                // any head's NaN makes the score NaN
+                const bool any = (__ballot_sync(0xffffffffu, nan[h]) >> (4 * gid)) & 15u;
+                const int j = j0 + gid + 8 * h;
+                if (tig == 0 && j < nb)
+                    p.keys[(((int64_t)b * p.t.T + tok) * p.c.nkv + g) * p.t.n_table + j] =
+                        ~order_key(any ? __uint_as_float(0x7fc00000u) : has[h] ? best[h] : -INFINITY);
+            }
+        }
+    }
     }
 }
 
-// One CTA per (sequence, token, kv head).
-__global__ void __launch_bounds__(kPickThreads) block_choose_kernel(const __grid_constant__ SelectParams p) {
-    __shared__ PickSmem sm;
+// One CTA per (sequence, token, kv head). ALL: the CTA holds every key (n_table <= THREADS KEYS);
+// else they are read again (from L2) for each digit and then in order, THREADS KEYS at a time.
+template <int THREADS, int KEYS, bool ALL>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) block_choose_kernel(const __grid_constant__ SelectParams p) {
+    __shared__ PickSmem<THREADS> sm;
+    const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const int64_t bt = row / p.c.nkv;
     const int b = (int)(bt / p.t.T), tok = (int)(bt % p.t.T);
-    const SeqStep s = seq_step(p.t, b);
+    const SeqStep s = seq_step(p.t, b);  // (written before the kernel that lets this one start)
+    pdl_wait();
     if (tok >= s.q) return;
     const int lim = s.len - s.q + tok + 1;
     const int nb = blocks_of(lim, p.c.bs, p.t.n_table);
-    if (threadIdx.x == 0 && lim > 0 && (lim - 1) / p.c.bs >= p.t.n_table) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
+    if (tid == 0 && lim > 0 && (lim - 1) / p.c.bs >= p.t.n_table) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
     int32_t* out = p.sel + row * p.n_sel;
-    for (int i = threadIdx.x; i < p.n_sel; i += kPickThreads)
+    for (int i = tid; i < p.n_sel; i += THREADS)
         if (i >= nb) out[i] = -1;
     if (nb <= p.n_sel) {
-        for (int i = threadIdx.x; i < nb; i += kPickThreads) out[i] = i;
+        for (int i = tid; i < nb; i += THREADS) out[i] = i;
         return;
     }
-    const float* score = p.score + row * p.t.n_table;
-    auto key = [&](int i) -> uint32_t {  // smaller is better; the forced blocks before all others
-        return i < p.n_first || i >= nb - p.n_last ? 0u : ~order_key(__ldcg(score + i));
+    const uint32_t* keys = p.keys + row * p.t.n_table;
+    auto load = [&](int base, uint32_t (&k)[KEYS]) {  // the forced blocks before all others
+#pragma unroll
+        for (int u = 0; u < KEYS; ++u) {
+            const int i = base + u * THREADS + tid;
+            k[u] = i < p.n_first || i >= nb - p.n_last ? 0u : keys[i];
+        }
     };
-    uint32_t thr;
-    int need;
-    pick_threshold(key, nb, p.n_sel, sm, &thr, &need);
-    pick_in_order(key, nb, thr, need, sm, [](int) { return 0; },
-                  [&](int i, bool taken, uint32_t before, int) {
-                      if (taken) out[before] = i;
-                  });
+    uint32_t k[KEYS], thr, need, before[KEYS], taken;
+    if (ALL) load(0, k);
+    pick_threshold<THREADS>([&](auto f) {
+        for (int base = 0; base < nb; base += THREADS * KEYS) {
+            if (!ALL) load(base, k);
+#pragma unroll
+            for (int u = 0; u < KEYS; ++u)
+                if (base + u * THREADS + tid < nb) f(k[u]);
+            if (ALL) break;
+        }
+    }, (uint32_t)p.n_sel, sm, &thr, &need);
+    int done = 0;  // picked so far, the last `need` of them among the keys equal to thr
+    for (int base = 0; base < nb && done < p.n_sel; base += THREADS * KEYS) {
+        if (!ALL) load(base, k);
+        pick_places<THREADS, KEYS>(k, nb - base, thr, need, sm, &taken, before);
+#pragma unroll
+        for (int u = 0; u < KEYS; ++u)
+            if ((taken >> u) & 1u) out[done + (int)before[u]] = base + u * THREADS + tid;
+        if (ALL) break;
+        // what this part took, and how many of the equal keys are left for the next
+        int lt = 0, eq = 0;
+#pragma unroll
+        for (int u = 0; u < KEYS; ++u)
+            if ((taken >> u) & 1u) k[u] == thr ? ++eq : ++lt;
+        done += block_sum<THREADS>(lt + eq, sm);
+        need -= (uint32_t)block_sum<THREADS>(eq, sm);
+    }
 }
 
 struct EvictParams {
@@ -154,52 +264,91 @@ struct EvictParams {
     int32_t* n_freed;
 };
 
-// One CTA per sequence.
-__global__ void __launch_bounds__(kPickThreads) block_evict_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ PickSmem sm;
+// One CTA per sequence, THREADS KEYS entries at a time (ALL: there are no more). A part's entries
+// are read before any of it is written, and no part writes past itself, so that the outputs may
+// be the inputs.
+template <int THREADS, int KEYS, bool ALL>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) block_evict_kernel(const __grid_constant__ EvictParams p) {
+    __shared__ PickSmem<THREADS> sm;
     const int b = blockIdx.x, tid = threadIdx.x;
     const int n = (int)p.n_table;
+    pdl_wait();
+    pdl_launch_dependents();
     const int len = max(p.lens[b], 0);
-    __syncthreads();  // (out_lens may be lens)
     const int nb = blocks_of(len, p.bs, n);
     const int go = max(nb - p.keep, 0);
-    const int64_t base = (int64_t)b * p.n_table;
-    const int32_t* table = p.table + base;
-    const float* mass = p.mass + base;
-    int32_t* out_table = p.out_table + base;
-    float* out_mass = p.out_mass + base;
-    int32_t* freed = p.freed + base;
-    struct Entry {
-        int32_t block;
-        float mass;
-    };
-    if (go > 0) {
-        auto key = [&](int i) -> uint32_t {  // smallest mass first; protected blocks last of all
-            return i < p.n_first || i >= nb - p.n_last ? 0xffffffffu : order_key(mass[i]);
-        };
-        uint32_t thr;
-        int need;
-        pick_threshold(key, nb, go, sm, &thr, &need);
-        pick_in_order(key, nb, thr, need, sm, [&](int i) { return Entry{table[i], mass[i]}; },
-                      [&](int i, bool taken, uint32_t before, Entry e) {
-                          if (taken) {
-                              freed[before] = e.block;
-                          } else {
-                              out_table[i - (int)before] = e.block;
-                              out_mass[i - (int)before] = e.mass;
-                          }
-                      });
-    } else {
-        for (int i = tid; i < nb; i += kPickThreads) {
-            out_table[i] = table[i];
-            out_mass[i] = mass[i];
+    const int64_t base_at = (int64_t)b * p.n_table;
+    const int32_t* table = p.table + base_at;
+    const float* mass = p.mass + base_at;
+    int32_t* out_table = p.out_table + base_at;
+    float* out_mass = p.out_mass + base_at;
+    int32_t* freed = p.freed + base_at;
+    auto load = [&](int base, uint32_t (&k)[KEYS]) {  // smallest mass first; protected blocks last of all
+#pragma unroll
+        for (int u = 0; u < KEYS; ++u) {
+            const int i = base + u * THREADS + tid;
+            k[u] = i < p.n_first || i >= nb - p.n_last ? 0xffffffffu : order_key(mass[i]);
         }
+    };
+    uint32_t k[KEYS], thr = 0, need = 0, before[KEYS] = {}, taken = 0;
+    if (ALL && go > 0) load(0, k);
+    __syncthreads();  // (out_lens may be lens)
+    if (go > 0)
+        pick_threshold<THREADS>([&](auto f) {
+            for (int base = 0; base < nb; base += THREADS * KEYS) {
+                if (!ALL) load(base, k);
+#pragma unroll
+                for (int u = 0; u < KEYS; ++u)
+                    if (base + u * THREADS + tid < nb) f(k[u]);
+                if (ALL) break;
+            }
+        }, (uint32_t)go, sm, &thr, &need);
+    int done = 0;
+    for (int base = 0; base < nb; base += THREADS * KEYS) {
+        if (go > 0) {
+            if (!ALL) load(base, k);
+            pick_places<THREADS, KEYS>(k, nb - base, thr, need, sm, &taken, before);
+        }
+        constexpr int G = KEYS < 4 ? KEYS : 4;  // entries in registers at a time
+#pragma unroll
+        for (int u0 = 0; u0 < KEYS; u0 += G) {
+            int32_t blk[G];
+            float m[G];
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                const int i = base + (u0 + u) * THREADS + tid;
+                blk[u] = i < nb ? table[i] : 0;
+                m[u] = i < nb ? mass[i] : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                const int i = base + (u0 + u) * THREADS + tid, gone = done + (int)before[u0 + u];
+                if (i >= nb) continue;
+                if ((taken >> (u0 + u)) & 1u) {
+                    freed[gone] = blk[u];
+                } else {
+                    out_table[i - gone] = blk[u];
+                    out_mass[i - gone] = m[u];
+                }
+            }
+        }
+        if (ALL || go == 0) {
+            if (ALL) break;
+            continue;
+        }
+        int lt = 0, eq = 0;
+#pragma unroll
+        for (int u = 0; u < KEYS; ++u)
+            if ((taken >> u) & 1u) k[u] == thr ? ++eq : ++lt;
+        done += block_sum<THREADS>(lt + eq, sm);
+        need -= (uint32_t)block_sum<THREADS>(eq, sm);
     }
-    for (int i = nb - go + tid; i < n; i += kPickThreads) {
+    for (int i = nb - go + tid; i < n; i += THREADS) {
         out_table[i] = -1;
         out_mass[i] = 0.f;
     }
-    for (int i = go + tid; i < n; i += kPickThreads) freed[i] = -1;
+    for (int i = go + tid; i < n; i += THREADS) freed[i] = -1;
     if (tid == 0) {
         p.out_lens[b] = len - go * p.bs;
         p.n_freed[b] = go;
@@ -209,25 +358,31 @@ __global__ void __launch_bounds__(kPickThreads) block_evict_kernel(const __grid_
 }  // namespace
 
 size_t block_select_ws_bytes(const BlockCache& c, int B, int T, int64_t n_table) {
-    return (((size_t)B * T * c.nkv * n_table * sizeof(float)) + 15) & ~(size_t)15;
+    return (((size_t)B * T * c.nkv * n_table * sizeof(uint32_t)) + 15) & ~(size_t)15;
 }
 
 cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const uint16_t* q,
                                 int64_t q_stride, int nq, int n_sel, int n_first, int n_last,
                                 int32_t* sel, void* ws, cudaStream_t s) {
-    SelectParams p{c, t, q, q_stride, nq / c.nkv, n_sel, n_first, n_last, sel, static_cast<float*>(ws)};
+    SelectParams p{c, t, q, q_stride, nq / c.nkv, n_sel, n_first, n_last, sel, static_cast<uint32_t*>(ws)};
     const int64_t rows = (int64_t)t.B * t.T * c.nkv;
     if (rows > INT32_MAX) return cudaErrorInvalidValue;
-    int64_t chunks = (t.n_table + kScThreads - 1) / kScThreads;
-    if (chunks > 1024) chunks = 1024;
-    const dim3 grid((unsigned)rows, (unsigned)chunks);
-    if (c.hd == 64) block_score_kernel<64><<<grid, kScThreads, 0, s>>>(p);
-    else if (c.hd == 128) block_score_kernel<128><<<grid, kScThreads, 0, s>>>(p);
-    else block_score_kernel<256><<<grid, kScThreads, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    // parts of 128 blocks; about eight CTAs per SM at most, each then with several
+    const int64_t heads = (int64_t)t.B * c.nkv;
+    int64_t parts = (t.n_table + kScThreads / 2 - 1) / (kScThreads / 2);
+    const int64_t cap = (148 * 8 + heads - 1) / heads;
+    if (parts > cap) parts = cap;
+    const dim3 grid((unsigned)parts, (unsigned)c.nkv, (unsigned)t.B);
+    cudaError_t e = c.hd == 64 ? launch_after(block_score_kernel<64>, grid, kScThreads, 0, s, p)
+                  : c.hd == 128 ? launch_after(block_score_kernel<128>, grid, kScThreads, 0, s, p)
+                                : launch_after(block_score_kernel<256>, grid, kScThreads, 0, s, p);
     if (e != cudaSuccess) return e;
-    block_choose_kernel<<<(unsigned)rows, kPickThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    const dim3 g2((unsigned)rows);
+    // the fewest threads and keys that hold the table
+    if (t.n_table <= 512) return launch_after(block_choose_kernel<256, 2, true>, g2, 256, 0, s, p);
+    if (t.n_table <= 2048) return launch_after(block_choose_kernel<1024, 2, true>, g2, 1024, 0, s, p);
+    if (t.n_table <= 8192) return launch_after(block_choose_kernel<1024, 8, true>, g2, 1024, 0, s, p);
+    return launch_after(block_choose_kernel<1024, 8, false>, g2, 1024, 0, s, p);
 }
 
 cudaError_t block_evict_launch(int B, const int32_t* table, int64_t n_table, const int32_t* seq_lens,
@@ -236,8 +391,11 @@ cudaError_t block_evict_launch(int B, const int32_t* table, int64_t n_table, con
                                int32_t* n_freed, cudaStream_t s) {
     EvictParams p{table, n_table, seq_lens, mass, bs, keep, n_first, n_last, out_table, out_lens,
                   out_mass, freed, n_freed};
-    block_evict_kernel<<<(unsigned)B, kPickThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)B);
+    if (n_table <= 512) return launch_after(block_evict_kernel<256, 2, true>, grid, 256, 0, s, p);
+    if (n_table <= 2048) return launch_after(block_evict_kernel<1024, 2, true>, grid, 1024, 0, s, p);
+    if (n_table <= 8192) return launch_after(block_evict_kernel<1024, 8, true>, grid, 1024, 0, s, p);
+    return launch_after(block_evict_kernel<1024, 8, false>, grid, 1024, 0, s, p);
 }
 
 }  // namespace mtp
