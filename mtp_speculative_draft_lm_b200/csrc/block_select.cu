@@ -7,6 +7,8 @@
 // scores are bound by reading the means (hd + 4 bytes per block and head): a warp takes 16
 // blocks of a head at a time, whose bytes are the A operand of mma.sync m16n8k32 as they come
 // (a lane's 16-byte loads, the K dimension permuted alike in q), for all of the step's tokens.
+// (On f16 instructions, bytes made f16 by permutes, it took 485 instead of 420 instructions per 16
+// blocks and two tokens; what is left is the epilogue.)
 // The choice is one CTA for each token and head, its keys in registers: a search for the last
 // chosen key, then one prefix sum that gives every chosen block its place in the ascending list.
 //
@@ -23,7 +25,7 @@ namespace mtp {
 namespace {
 
 constexpr int kScThreads = 256;
-constexpr int kScRows = 128;  // query rows in 8 bits (padded groups) at a time
+constexpr int kScRows = 64;  // query rows in 8 bits (padded groups) at a time
 
 // Sum over the block's threads, in every one of them.
 template <int THREADS>
@@ -61,134 +63,133 @@ __host__ __device__ constexpr int q8_pitch() { return HD == 64 ? 64 : HD + 64; }
 // Rows a token takes there: its group, padded to the matrix unit's 8 columns.
 __host__ __device__ inline int group_rows(int group) { return (group + 7) & ~7; }
 
-// Grid (parts of the blocks, kv heads, sequences). The query rows are quantized to shared
+// Grid (kv heads, parts of the blocks, sequences). The query rows are quantized to shared
 // memory up to kScRows at a time; a warp has the next tile's blocks looked up while it waits for
 // this tile's means.
 template <int HD>
 __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_constant__ SelectParams p) {
     constexpr int C = HD / 64;  // 16-byte chunks of a lane, 64 bytes apart
     __shared__ __align__(16) uint8_t q8[kScRows * q8_pitch<HD>()];
-    __shared__ float sq[kScRows];
-    const int g = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(16) float2 sq[kScRows];  // scale; 0, or -infinity where the row does not count
+    const int g = blockIdx.x, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
     const SeqStep s = seq_step(p.t, b);
     const int nb = blocks_of(s.len, p.c.bs, p.t.n_table);
-    if (s.q == 0 || (int)blockIdx.x * (kScThreads / 2) >= nb) return;
+    if (s.q == 0 || (int)blockIdx.y * (kScThreads / 2) >= nb) return;
     const int gr = group_rows(p.group), chunk = kScRows / gr;  // tokens at a time
     const int gid = lane >> 2, tig = lane & 3;
-    const int j_first = ((int)blockIdx.x * (kScThreads / 32) + warp) * 16, j_step = (int)gridDim.x * (kScThreads / 2);
-    // blocks j + gid and j + gid + 8
-    auto look_up = [&](int j, int (&n)[2]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) n[h] = j + gid + 8 * h < nb ? table_block(p.t, p.c.num_blocks, b, j + gid + 8 * h) : -1;
-    };
-    for (int t0 = 0; t0 < s.q; t0 += chunk) {
-    const int t1 = min(s.q, t0 + chunk), rows = (t1 - t0) * gr;
-    int next[2];
-    look_up(j_first, next);
-    if (t0) __syncthreads();  // the earlier rows have been used
-    for (int r = warp; r < rows; r += kScThreads / 32) {
-        const int tok = t0 + r / gr, i = r % gr;
-        const bool has = i < p.group;
-        float v[HD / 32], mx = 0.f;
-        bool odd = !has;  // no head, or one with an infinity or NaN
-        if (has) {
-            const uint16_t* src = p.q + ((int64_t)b * p.t.T + tok) * p.q_stride + ((int64_t)g * p.group + i) * HD + lane * (HD / 32);
-            if constexpr (HD == 64) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(src);
-                v[0] = bf16_lo(w), v[1] = bf16_hi(w);
-            } else {
-#pragma unroll
-                for (int u = 0; u < HD / 128; ++u) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(src + 4 * u);
-                    v[4 * u] = bf16_lo(w.x), v[4 * u + 1] = bf16_hi(w.x), v[4 * u + 2] = bf16_lo(w.y), v[4 * u + 3] = bf16_hi(w.y);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < HD / 32; ++k) {
-                mx = fmaxf(mx, fabsf(v[k]));
-                odd = odd || !(fabsf(v[k]) < INFINITY);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < HD / 32; ++k) v[k] = 0.f;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        odd = __any_sync(0xffffffffu, odd);
-        const float sc = __fmul_rn(mx, kInv127);
-        uint32_t w[(HD / 32 + 3) / 4] = {};
-        if (!odd && sc > 0.f)
-#pragma unroll
-            for (int k = 0; k < HD / 32; ++k)
-                w[k >> 2] |= ((uint32_t)__float2int_rn(__fdiv_rn(v[k], sc)) & 255u) << (8 * (k & 3));
-        uint8_t* dst = q8 + r * q8_pitch<HD>() + lane * (HD / 32);
-        if constexpr (HD == 64) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
-        else
-#pragma unroll
-            for (int u = 0; u < HD / 128; ++u) reinterpret_cast<uint32_t*>(dst)[u] = w[u];
-        if (lane == 0) sq[r] = odd ? -1.f : sc;
-    }
-    __syncthreads();
-    for (int j0 = j_first; j0 < nb; j0 += j_step) {
-        // rows gid and gid + 8 of the tile: blocks j0 + gid and 8 on
-        uint4 m[2][C];
-        float sk[2];
-        bool has[2];
+    const int j_first = ((int)blockIdx.y * (kScThreads / 32) + warp) * 16, j_step = (int)gridDim.y * (kScThreads / 2);
+    const int32_t* table = p.t.table + (int64_t)b * p.t.n_table;
+    const uint32_t blocks = (uint32_t)p.c.num_blocks;
+    auto look_up = [&](int j, int (&n)[2]) {  // blocks j + gid and j + gid + 8 (-1: none)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int j = j0 + gid + 8 * h;
-            const int n = next[h];
-            has[h] = n >= 0;
-            if (j < nb && n < 0 && tig == 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
-            sk[h] = 0.f;
-#pragma unroll
-            for (int c = 0; c < C; ++c) m[h][c] = make_uint4(0, 0, 0, 0);
-            if (has[h]) {
-                const int64_t at = (int64_t)n * p.c.nkv + g;
-                sk[h] = p.c.k_mean_scale[at];
-#pragma unroll
-                for (int c = 0; c < C; ++c) m[h][c] = *reinterpret_cast<const uint4*>(p.c.k_mean + at * HD + 64 * c + 16 * tig);
+            n[h] = j + gid + 8 * h < nb ? __ldg(table + j + gid + 8 * h) : -1;
+            if ((uint32_t)n[h] >= blocks) {
+                if (j + gid + 8 * h < nb && tig == 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
+                n[h] = -1;
             }
         }
-        look_up(j0 + j_step, next);
-        for (int tok = t0; tok < t1; ++tok) {
-            float best[2] = {-INFINITY, -INFINITY};
-            bool nan[2] = {false, false};
-            for (int r0 = (tok - t0) * gr; r0 < (tok - t0 + 1) * gr; r0 += 8) {
-                int d[4] = {0, 0, 0, 0};
+    };
+    for (int t0 = 0; t0 < s.q; t0 += chunk) {
+        const int t1 = min(s.q, t0 + chunk), rows = (t1 - t0) * gr;
+        int next[2];
+        look_up(j_first, next);
+        if (t0) __syncthreads();  // the earlier rows have been used
+        for (int r = warp; r < rows; r += kScThreads / 32) {
+            const int tok = t0 + r / gr, i = r % gr;
+            const bool has = i < p.group;
+            float v[HD / 32], mx = 0.f;
+            bool odd = !has;  // no head, or one with an infinity or NaN
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(q8 + (r0 + gid) * q8_pitch<HD>() + 64 * c + 16 * tig);
-                    mma_s8(d, m[0][c].x, m[1][c].x, m[0][c].y, m[1][c].y, q.x, q.y);
-                    mma_s8(d, m[0][c].z, m[1][c].z, m[0][c].w, m[1][c].w, q.z, q.w);
+            for (int k = 0; k < HD / 32; ++k) v[k] = 0.f;
+            if (has) {
+                const uint16_t* src = p.q + ((int64_t)b * p.t.T + tok) * p.q_stride + ((int64_t)g * p.group + i) * HD + lane * (HD / 32);
+#pragma unroll
+                for (int k = 0; k < HD / 32; k += 2) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + k);
+                    v[k] = bf16_lo(w), v[k + 1] = bf16_hi(w);
+                    mx = fmaxf(mx, fmaxf(fabsf(v[k]), fabsf(v[k + 1])));
+                    odd = odd || !(fabsf(v[k]) < INFINITY) || !(fabsf(v[k + 1]) < INFINITY);
                 }
-                const float2 sc = *reinterpret_cast<const float2*>(sq + r0 + 2 * tig);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = __fmul_rn((float)d[2 * h + e], __fmul_rn(e ? sc.y : sc.x, sk[h]));
-                        if ((e ? sc.y : sc.x) >= 0.f) {
-                            nan[h] = nan[h] || f != f;
-                            best[h] = fmaxf(best[h], f);
-                        }
-                    }
             }
+            mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));  // (not negative)
+            odd = __any_sync(0xffffffffu, odd);
+            const float sc = __fmul_rn(mx, kInv127);
+            uint32_t w[(HD / 32 + 3) / 4] = {};
+            if (!odd && sc > 0.f)
+#pragma unroll
+                for (int k = 0; k < HD / 32; ++k)
+                    w[k >> 2] |= ((uint32_t)__float2int_rn(__fdiv_rn(v[k], sc)) & 255u) << (8 * (k & 3));
+            uint8_t* dst = q8 + r * q8_pitch<HD>() + lane * (HD / 32);
+            if constexpr (HD == 64) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
+            else
+#pragma unroll
+                for (int u = 0; u < HD / 128; ++u) reinterpret_cast<uint32_t*>(dst)[u] = w[u];
+            if (lane == 0) sq[r] = odd ? make_float2(0.f, -INFINITY) : make_float2(sc, 0.f);
+        }
+        __syncthreads();
+        for (int j0 = j_first; j0 < nb; j0 += j_step) {
+            // rows gid and gid + 8 of the tile: blocks j0 + gid and 8 on
+            uint4 m[2][C];
+            float sk[2];
+            const bool has[2] = {next[0] >= 0, next[1] >= 0};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 1));
-                best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], 2));
-                // any head's NaN makes the score NaN
-                const bool any = (__ballot_sync(0xffffffffu, nan[h]) >> (4 * gid)) & 15u;
-                const int j = j0 + gid + 8 * h;
-                if (tig == 0 && j < nb)
-                    p.keys[(((int64_t)b * p.t.T + tok) * p.c.nkv + g) * p.t.n_table + j] =
-                        ~order_key(any ? __uint_as_float(0x7fc00000u) : has[h] ? best[h] : -INFINITY);
+                sk[h] = 0.f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) m[h][c] = make_uint4(0, 0, 0, 0);
+                if (has[h]) {
+                    const int64_t at = (int64_t)next[h] * p.c.nkv + g;
+                    sk[h] = p.c.k_mean_scale[at];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) m[h][c] = ldg_stream(p.c.k_mean + at * HD + 64 * c + 16 * tig);
+                }
+            }
+            look_up(j0 + j_step, next);
+            // lane tig 0 writes block j0 + gid, lane 1 block j0 + gid + 8
+            const int j = j0 + gid + 8 * (tig & 1);
+            uint32_t* out = p.keys + (((int64_t)b * p.t.T + t0) * p.c.nkv + g) * p.t.n_table + j;
+            const bool writes = tig < 2 && j < nb, there = tig & 1 ? has[1] : has[0];
+            for (int r1 = 0; r1 < rows; r1 += gr) {
+                float best[2] = {-INFINITY, -INFINITY};
+                bool nan[2] = {false, false};
+                for (int r0 = r1; r0 < r1 + gr; r0 += 8) {
+                    // sums onto 1.5 2^23 as fp32 bits: below 2^22, they are that float's units
+                    int d[4] = {0x4B400000, 0x4B400000, 0x4B400000, 0x4B400000};
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const uint4 q = *reinterpret_cast<const uint4*>(q8 + (r0 + gid) * q8_pitch<HD>() + 64 * c + 16 * tig);
+                        mma_s8(d, m[0][c].x, m[1][c].x, m[0][c].y, m[1][c].y, q.x, q.y);
+                        mma_s8(d, m[0][c].z, m[1][c].z, m[0][c].w, m[1][c].w, q.z, q.w);
+                    }
+                    const float4 sc = *reinterpret_cast<const float4*>(&sq[r0 + 2 * tig]);  // rows 2 tig, 2 tig + 1
+                    float f[2][2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f[h][0] = __fmul_rn(__int_as_float(d[2 * h]) - 12582912.f, __fmul_rn(sc.x, sk[h]));
+                        f[h][1] = __fmul_rn(__int_as_float(d[2 * h + 1]) - 12582912.f, __fmul_rn(sc.z, sk[h]));
+                        best[h] = fmaxf(best[h], fmaxf(f[h][0] + sc.y, f[h][1] + sc.w));
+                    }
+                    // a NaN (of a mean's scale, or 0 times an overflown product): which rows have one
+                    const float any = (f[0][0] + f[0][1]) + (f[1][0] + f[1][1]);
+                    if (__any_sync(0xffffffffu, any != any))
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const bool mine = (sc.y == 0.f && f[h][0] != f[h][0]) || (sc.w == 0.f && f[h][1] != f[h][1]);
+                            nan[h] = nan[h] || ((__ballot_sync(0xffffffffu, mine) >> (4 * gid)) & 15u);
+                        }
+                }
+                // the largest over the four lanes of a row, each lane going on with one of the two rows
+                const bool hi = tig & 1;
+                float v = fmaxf(hi ? best[1] : best[0], __shfl_xor_sync(0xffffffffu, hi ? best[0] : best[1], 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                if (hi ? nan[1] : nan[0]) v = __uint_as_float(0x7fc00000u);
+                if (writes) *out = ~order_key(there ? v : -INFINITY);
+                out += (int64_t)p.c.nkv * p.t.n_table;
             }
         }
-    }
     }
 }
 
@@ -372,7 +373,7 @@ cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const 
     int64_t parts = (t.n_table + kScThreads / 2 - 1) / (kScThreads / 2);
     const int64_t cap = (148 * 8 + heads - 1) / heads;
     if (parts > cap) parts = cap;
-    const dim3 grid((unsigned)parts, (unsigned)c.nkv, (unsigned)t.B);
+    const dim3 grid((unsigned)c.nkv, (unsigned)parts, (unsigned)t.B);
     cudaError_t e = c.hd == 64 ? launch_after(block_score_kernel<64>, grid, kScThreads, 0, s, p)
                   : c.hd == 128 ? launch_after(block_score_kernel<128>, grid, kScThreads, 0, s, p)
                                 : launch_after(block_score_kernel<256>, grid, kScThreads, 0, s, p);
