@@ -4,7 +4,7 @@
 // heads, of an 8-bit dot product with the block's mean key. The dot is a whole number (127 127
 // 256 < 2^24, as fp32 exact) and each fp32 step is rounded to nearest, so the scores, and with
 // them the chosen blocks, are the same bits everywhere; ties go to the lowest index. The
-// scores are bound by reading the means (hd + 4 bytes per block and head): a warp takes 16
+// scores are bound by reading the means (hd + 4 bytes per block and head): a warp takes 32
 // blocks of a head at a time, whose bytes are the A operand of mma.sync m16n8k32 as they come
 // (a lane's 16-byte loads, the K dimension permuted alike in q), for all of the step's tokens.
 // (On f16 instructions, bytes made f16 by permutes, it took 485 instead of 420 instructions per 16
@@ -25,6 +25,8 @@ namespace mtp {
 namespace {
 
 constexpr int kScThreads = 256;
+constexpr int kPartBlocks = kScThreads / 32 * 32;  // blocks that a CTA's warps score at a time
+constexpr int kMostRounds = 4;
 constexpr int kScRows = 64;  // query rows in 8 bits (padded groups) at a time
 
 // Sum over the block's threads, in every one of them.
@@ -47,6 +49,7 @@ struct SelectParams {
     int n_sel, n_first, n_last;
     int32_t* sel;
     uint32_t* keys;  // [B, T, nkv, n_table]: the score's order, smallest best
+    int part;        // blocks of a CTA (the score's): a multiple of kPartBlocks
 };
 
 // D[16 x 8] += A[16 x 32] B[32 x 8], 8-bit integers.
@@ -60,8 +63,7 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 // Bytes between the 8-bit query rows in shared memory: two rows' 64-byte pieces in other banks.
 template <int HD>
 __host__ __device__ constexpr int q8_pitch() { return HD == 64 ? 64 : HD + 64; }
-// Rows a token takes there: its group, padded to the matrix unit's 8 columns.
-__host__ __device__ inline int group_rows(int group) { return (group + 7) & ~7; }
+// (A token takes 8 or 16 rows there: its group, padded to the matrix unit's columns.)
 
 // Grid (kv heads, parts of the blocks, sequences). The query rows are quantized to shared
 // memory up to kScRows at a time; a warp has the next tile's blocks looked up while it waits for
@@ -76,15 +78,20 @@ __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_co
     pdl_launch_dependents();
     const SeqStep s = seq_step(p.t, b);
     const int nb = blocks_of(s.len, p.c.bs, p.t.n_table);
-    if (s.q == 0 || (int)blockIdx.y * (kScThreads / 2) >= nb) return;
-    const int gr = group_rows(p.group), chunk = kScRows / gr;  // tokens at a time
+    const int part0 = (int)blockIdx.y * p.part;
+    if (s.q == 0 || part0 >= nb) return;
+    const int gr_log = p.group > 8 ? 4 : 3, gr = 1 << gr_log, chunk = kScRows >> gr_log;  // a token's rows; tokens at a time
     const int gid = lane >> 2, tig = lane & 3;
-    const int j_first = ((int)blockIdx.y * (kScThreads / 32) + warp) * 16, j_step = (int)gridDim.y * (kScThreads / 2);
+    const int j_first = part0 + warp * 32, j_end = min(nb, part0 + p.part);
+    uint32_t* const keys = p.keys + ((int64_t)b * p.t.T * p.c.nkv + g) * p.t.n_table;
+    const int64_t key_step = (int64_t)p.c.nkv * p.t.n_table;
+    const int8_t* const means = p.c.k_mean + (int64_t)g * HD + 16 * tig;
+    const float* const scales = p.c.k_mean_scale + g;
     const int32_t* table = p.t.table + (int64_t)b * p.t.n_table;
     const uint32_t blocks = (uint32_t)p.c.num_blocks;
-    auto look_up = [&](int j, int (&n)[2]) {  // blocks j + gid and j + gid + 8 (-1: none)
+    auto look_up = [&](int j, int (&n)[4]) {  // blocks j + gid + 8 h (-1: none)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
             n[h] = j + gid + 8 * h < nb ? __ldg(table + j + gid + 8 * h) : -1;
             if ((uint32_t)n[h] >= blocks) {
                 if (j + gid + 8 * h < nb && tig == 0) raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);
@@ -94,100 +101,107 @@ __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_co
     };
     for (int t0 = 0; t0 < s.q; t0 += chunk) {
         const int t1 = min(s.q, t0 + chunk), rows = (t1 - t0) * gr;
-        int next[2];
+        int next[4];
         look_up(j_first, next);
         if (t0) __syncthreads();  // the earlier rows have been used
-        for (int r = warp; r < rows; r += kScThreads / 32) {
-            const int tok = t0 + r / gr, i = r % gr;
+        // HD / 8 lanes per row, 8 values each: one load and one pass for 16 rows of 128
+        constexpr int LPR = HD / 8, RPW = 32 / LPR;
+        for (int r = warp * RPW + lane / LPR; r < rows; r += kScThreads / 32 * RPW) {  // (whole warps: rows is a multiple of 8)
+            const int tok = t0 + (r >> gr_log), i = r & (gr - 1), l = lane % LPR;
             const bool has = i < p.group;
-            float v[HD / 32], mx = 0.f;
-            bool odd = !has;  // no head, or one with an infinity or NaN
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (has) x = *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.t.T + tok) * p.q_stride + ((int64_t)g * p.group + i) * HD + 8 * l);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+            uint32_t top = 0;  // the largest magnitude's bits: infinities and NaN above all others
 #pragma unroll
-            for (int k = 0; k < HD / 32; ++k) v[k] = 0.f;
-            if (has) {
-                const uint16_t* src = p.q + ((int64_t)b * p.t.T + tok) * p.q_stride + ((int64_t)g * p.group + i) * HD + lane * (HD / 32);
+            for (int k = 0; k < 4; ++k) top = __vmaxu2(top, xw[k] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-                for (int k = 0; k < HD / 32; k += 2) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + k);
-                    v[k] = bf16_lo(w), v[k + 1] = bf16_hi(w);
-                    mx = fmaxf(mx, fmaxf(fabsf(v[k]), fabsf(v[k + 1])));
-                    odd = odd || !(fabsf(v[k]) < INFINITY) || !(fabsf(v[k + 1]) < INFINITY);
-                }
+            for (int o = LPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool odd = !has || top >= 0x7f80u;  // no head, or one with an infinity or NaN
+            const float sc = odd ? 0.f : __fmul_rn(bf16_to_f32((uint16_t)top), kInv127);
+            // rint(v / sc): by the reciprocal, and by the division itself where that is within
+            // 10^-4 of a half (its error is below 3 10^-5) or the scale is tiny
+            const bool tiny = sc < 1e-30f;
+            const float inv = tiny ? 0.f : __fdiv_rn(1.f, sc);
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float v = k & 1 ? bf16_hi(xw[k >> 1]) : bf16_lo(xw[k >> 1]);
+                float n = rintf(v * inv);
+                if (sc > 0.f && (tiny || fabsf(fabsf(v * inv - n) - 0.5f) < 1e-4f)) n = rintf(__fdiv_rn(v, sc));
+                w[k >> 2] |= ((uint32_t)(int)n & 255u) << (8 * (k & 3));
             }
-            mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));  // (not negative)
-            odd = __any_sync(0xffffffffu, odd);
-            const float sc = __fmul_rn(mx, kInv127);
-            uint32_t w[(HD / 32 + 3) / 4] = {};
-            if (!odd && sc > 0.f)
-#pragma unroll
-                for (int k = 0; k < HD / 32; ++k)
-                    w[k >> 2] |= ((uint32_t)__float2int_rn(__fdiv_rn(v[k], sc)) & 255u) << (8 * (k & 3));
-            uint8_t* dst = q8 + r * q8_pitch<HD>() + lane * (HD / 32);
-            if constexpr (HD == 64) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w[0];
-            else
-#pragma unroll
-                for (int u = 0; u < HD / 128; ++u) reinterpret_cast<uint32_t*>(dst)[u] = w[u];
-            if (lane == 0) sq[r] = odd ? make_float2(0.f, -INFINITY) : make_float2(sc, 0.f);
+            if (!(sc > 0.f)) w[0] = w[1] = 0;
+            *reinterpret_cast<uint2*>(q8 + r * q8_pitch<HD>() + 8 * l) = make_uint2(w[0], w[1]);
+            if (l == 0) sq[r] = odd ? make_float2(0.f, -INFINITY) : make_float2(sc, 0.f);
         }
         __syncthreads();
-        for (int j0 = j_first; j0 < nb; j0 += j_step) {
-            // rows gid and gid + 8 of the tile: blocks j0 + gid and 8 on
-            uint4 m[2][C];
-            float sk[2];
-            const bool has[2] = {next[0] >= 0, next[1] >= 0};
+        for (int j0 = j_first; j0 < j_end; j0 += kPartBlocks) {
+            // two tiles of 16 blocks; rows gid and gid + 8 of tile u: blocks j0 + gid + 8 (2 u + {0, 1})
+            uint4 m[4][C];
+            float sk[4];
+            uint32_t has = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 4; ++h) {
                 sk[h] = 0.f;
 #pragma unroll
                 for (int c = 0; c < C; ++c) m[h][c] = make_uint4(0, 0, 0, 0);
-                if (has[h]) {
-                    const int64_t at = (int64_t)next[h] * p.c.nkv + g;
-                    sk[h] = p.c.k_mean_scale[at];
+                if (next[h] >= 0) {
+                    has |= 1u << h;
+                    const int64_t at = (int64_t)next[h] * p.c.nkv;
+                    sk[h] = scales[at];
 #pragma unroll
-                    for (int c = 0; c < C; ++c) m[h][c] = ldg_stream(p.c.k_mean + at * HD + 64 * c + 16 * tig);
+                    for (int c = 0; c < C; ++c) m[h][c] = ldg_stream(means + at * HD + 64 * c);
                 }
             }
-            look_up(j0 + j_step, next);
-            // lane tig 0 writes block j0 + gid, lane 1 block j0 + gid + 8
-            const int j = j0 + gid + 8 * (tig & 1);
-            uint32_t* out = p.keys + (((int64_t)b * p.t.T + t0) * p.c.nkv + g) * p.t.n_table + j;
-            const bool writes = tig < 2 && j < nb, there = tig & 1 ? has[1] : has[0];
+            if (j0 + kPartBlocks < j_end) look_up(j0 + kPartBlocks, next);
+            // lane tig of a row's four writes block j0 + gid + 8 tig
+            const int j = j0 + gid + 8 * tig;
+            uint32_t* out = keys + t0 * key_step + j;
+            const bool there = (has >> tig) & 1u;
             for (int r1 = 0; r1 < rows; r1 += gr) {
-                float best[2] = {-INFINITY, -INFINITY};
-                bool nan[2] = {false, false};
+                float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                uint32_t nan = 0;  // rows (bit h) with a NaN
                 for (int r0 = r1; r0 < r1 + gr; r0 += 8) {
                     // sums onto 1.5 2^23 as fp32 bits: below 2^22, they are that float's units
-                    int d[4] = {0x4B400000, 0x4B400000, 0x4B400000, 0x4B400000};
+                    int d[2][4];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) d[k >> 2][k & 3] = 0x4B400000;
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         const uint4 q = *reinterpret_cast<const uint4*>(q8 + (r0 + gid) * q8_pitch<HD>() + 64 * c + 16 * tig);
-                        mma_s8(d, m[0][c].x, m[1][c].x, m[0][c].y, m[1][c].y, q.x, q.y);
-                        mma_s8(d, m[0][c].z, m[1][c].z, m[0][c].w, m[1][c].w, q.z, q.w);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            mma_s8(d[u], m[2 * u][c].x, m[2 * u + 1][c].x, m[2 * u][c].y, m[2 * u + 1][c].y, q.x, q.y);
+                            mma_s8(d[u], m[2 * u][c].z, m[2 * u + 1][c].z, m[2 * u][c].w, m[2 * u + 1][c].w, q.z, q.w);
+                        }
                     }
                     const float4 sc = *reinterpret_cast<const float4*>(&sq[r0 + 2 * tig]);  // rows 2 tig, 2 tig + 1
-                    float f[2][2];
+                    float f[4][2], any = 0.f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        f[h][0] = __fmul_rn(__int_as_float(d[2 * h]) - 12582912.f, __fmul_rn(sc.x, sk[h]));
-                        f[h][1] = __fmul_rn(__int_as_float(d[2 * h + 1]) - 12582912.f, __fmul_rn(sc.z, sk[h]));
+                    for (int h = 0; h < 4; ++h) {
+                        f[h][0] = __fmul_rn(__int_as_float(d[h >> 1][2 * (h & 1)]) - 12582912.f, __fmul_rn(sc.x, sk[h]));
+                        f[h][1] = __fmul_rn(__int_as_float(d[h >> 1][2 * (h & 1) + 1]) - 12582912.f, __fmul_rn(sc.z, sk[h]));
                         best[h] = fmaxf(best[h], fmaxf(f[h][0] + sc.y, f[h][1] + sc.w));
+                        any += f[h][0] + f[h][1];
                     }
                     // a NaN (of a mean's scale, or 0 times an overflown product): which rows have one
-                    const float any = (f[0][0] + f[0][1]) + (f[1][0] + f[1][1]);
                     if (__any_sync(0xffffffffu, any != any))
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < 4; ++h) {
                             const bool mine = (sc.y == 0.f && f[h][0] != f[h][0]) || (sc.w == 0.f && f[h][1] != f[h][1]);
-                            nan[h] = nan[h] || ((__ballot_sync(0xffffffffu, mine) >> (4 * gid)) & 15u);
+                            if ((__ballot_sync(0xffffffffu, mine) >> (4 * gid)) & 15u) nan |= 1u << h;
                         }
                 }
-                // the largest over the four lanes of a row, each lane going on with one of the two rows
-                const bool hi = tig & 1;
-                float v = fmaxf(hi ? best[1] : best[0], __shfl_xor_sync(0xffffffffu, hi ? best[0] : best[1], 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                if (hi ? nan[1] : nan[0]) v = __uint_as_float(0x7fc00000u);
-                if (writes) *out = ~order_key(there ? v : -INFINITY);
-                out += (int64_t)p.c.nkv * p.t.n_table;
+                // the largest over a row's four lanes, lane tig going on with row h = tig
+                const bool h2 = tig & 2, h1 = tig & 1;
+                const float a0 = fmaxf(h2 ? best[2] : best[0], __shfl_xor_sync(0xffffffffu, h2 ? best[0] : best[2], 2));
+                const float a1 = fmaxf(h2 ? best[3] : best[1], __shfl_xor_sync(0xffffffffu, h2 ? best[1] : best[3], 2));
+                float v = fmaxf(h1 ? a1 : a0, __shfl_xor_sync(0xffffffffu, h1 ? a0 : a1, 1));
+                if ((nan >> tig) & 1u) v = __uint_as_float(0x7fc00000u);
+                if (j < j_end) *out = ~order_key(there ? v : -INFINITY);
+                out += key_step;
             }
         }
     }
@@ -365,14 +379,14 @@ size_t block_select_ws_bytes(const BlockCache& c, int B, int T, int64_t n_table)
 cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const uint16_t* q,
                                 int64_t q_stride, int nq, int n_sel, int n_first, int n_last,
                                 int32_t* sel, void* ws, cudaStream_t s) {
-    SelectParams p{c, t, q, q_stride, nq / c.nkv, n_sel, n_first, n_last, sel, static_cast<uint32_t*>(ws)};
+    SelectParams p{c, t, q, q_stride, nq / c.nkv, n_sel, n_first, n_last, sel, static_cast<uint32_t*>(ws), 0};
     const int64_t rows = (int64_t)t.B * t.T * c.nkv;
     if (rows > INT32_MAX) return cudaErrorInvalidValue;
-    // parts of 128 blocks; about eight CTAs per SM at most, each then with several
-    const int64_t heads = (int64_t)t.B * c.nkv;
-    int64_t parts = (t.n_table + kScThreads / 2 - 1) / (kScThreads / 2);
-    const int64_t cap = (148 * 8 + heads - 1) / heads;
-    if (parts > cap) parts = cap;
+    // a CTA's blocks: as many as leave about four CTAs per SM, at most kMostRounds rounds of its warps
+    const int64_t rounds = t.n_table * t.B * c.nkv / ((int64_t)kPartBlocks * 148 * 4);
+    p.part = kPartBlocks * (int)(rounds < 1 ? 1 : rounds > kMostRounds ? kMostRounds : rounds);
+    const int64_t parts = (t.n_table + p.part - 1) / p.part;
+    if (parts > 65535) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)c.nkv, (unsigned)parts, (unsigned)t.B);
     cudaError_t e = c.hd == 64 ? launch_after(block_score_kernel<64>, grid, kScThreads, 0, s, p)
                   : c.hd == 128 ? launch_after(block_score_kernel<128>, grid, kScThreads, 0, s, p)
