@@ -158,11 +158,26 @@ def _ptr(a):
     return a.data_ptr()
 
 
+_current_stream = None  # () -> torch's current stream on the current device, as an address
+
+
+def _find_current_stream():
+    import torch
+
+    if not torch.cuda.is_available():
+        return lambda: None
+    torch.cuda.init()
+    # (the address alone: building torch's Stream object takes 6 us, more than a launch)
+    device, raw = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+    return lambda: raw(device())
+
+
 def _stream(s):
     if s is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -266,6 +266,7 @@ class BlockCache:
     k_mean: torch.Tensor | None = None
     k_mean_scale: torch.Tensor | None = None
     desc: L.mtp_block_cache = field(init=False)
+    ws_bytes: dict = field(init=False, default_factory=dict, repr=False)  # workspace sizes asked for
 
     def __post_init__(self):
         nb, nkv, bs, hd = self.k.shape
@@ -307,17 +308,21 @@ class BlockCache:
 
 def _token_stride(x: torch.Tensor) -> int:
     """Elements between the tokens of x [B, T, heads, hd], whose heads are packed."""
-    B, T, _, hd = x.shape
+    B, T, n, hd = x.shape
     st = x.stride()
-    if x.dtype != torch.bfloat16 or st[3] != 1 or (x.shape[2] > 1 and st[2] != hd):
+    if x.dtype is not torch.bfloat16 or st[3] != 1 or (n > 1 and st[2] != hd):
         raise ValueError("expected bf16 [B, T, heads, hd] with packed heads")
-    step = st[1] if T > 1 else st[0] if B > 1 else x.shape[2] * hd
+    step = st[1] if T > 1 else st[0] if B > 1 else n * hd
     if B > 1 and st[0] != T * step:
         raise ValueError("sequences must be T token strides apart")
     return step
 
 
-def _block_ws(ws, nbytes: int, device):
+def _block_ws(cache: BlockCache, ws, size, key: tuple, device):
+    """ws if it is large enough, else a new one; size(desc, *key) says how large (asked once per key)."""
+    nbytes = cache.ws_bytes.get((size, key))
+    if nbytes is None:
+        nbytes = cache.ws_bytes[size, key] = size(cache.desc, *key)
     return torch.empty((nbytes,), dtype=torch.uint8, device=device) if ws is None or ws.numel() < nbytes else ws
 
 
@@ -325,11 +330,11 @@ def block_append(cache: BlockCache, k, v, block_table, seq_lens, q_lens=None, de
                  stream=None):
     """Writes the new rows k, v [B, T, nkv, hd] (bf16, slices of a projection allowed) at the end
     of each sequence (seq_lens counts them already) and updates scales and means."""
-    B, T = k.shape[:2]
-    step = _token_stride(k)
-    if k.shape != v.shape or _token_stride(v) != step or k.shape[2] != cache.desc.nkv or k.shape[3] != cache.desc.hd:
+    B, T, n, hd = k.shape
+    step, d = _token_stride(k), cache.desc
+    if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride() or n != d.nkv or hd != d.hd:
         raise ValueError("k and v must be the cache's heads with one stride")
-    L.mtp_block_append(cache.desc, k, v, step, B, T, seq_lens, q_lens, block_table,
+    L.mtp_block_append(d, k, v, step, B, T, seq_lens, q_lens, block_table,
                        block_table.shape[1], dev_err, stream)
 
 
@@ -340,7 +345,7 @@ def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=N
     B, T, nq, hd = q.shape
     out = torch.empty((B, T, nq, hd), dtype=torch.bfloat16, device=q.device) if out is None else out
     n_table = block_table.shape[1]
-    ws = _block_ws(ws, L.mtp_block_attn_ws_bytes(cache.desc, B, T, nq, n_table, out_mass is not None), q.device)
+    ws = _block_ws(cache, ws, L.mtp_block_attn_ws_bytes, (B, T, nq, n_table, out_mass is not None), q.device)
     L.mtp_block_attn(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table, n_table,
                      1.0 / float(hd) ** 0.5 if scale is None else scale, out, out_lse, mass, out_mass,
                      dev_err, ws, ws.numel(), stream)
@@ -354,7 +359,7 @@ def block_select(cache: BlockCache, q, block_table, seq_lens, n_sel, n_first=1, 
     B, T, nq, _ = q.shape
     n_table = block_table.shape[1]
     out = torch.empty((B, T, cache.desc.nkv, n_sel), dtype=torch.int32, device=q.device) if out is None else out
-    ws = _block_ws(ws, L.mtp_block_select_ws_bytes(cache.desc, B, T, n_table), q.device)
+    ws = _block_ws(cache, ws, L.mtp_block_select_ws_bytes, (B, T, n_table), q.device)
     L.mtp_block_select(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table, n_table,
                        n_sel, n_first, n_last, out, dev_err, ws, ws.numel(), stream)
     return out, ws
@@ -366,7 +371,7 @@ def block_sparse_attn(cache: BlockCache, q, block_table, seq_lens, sel, q_lens=N
     B, T, nq, hd = q.shape
     out = torch.empty((B, T, nq, hd), dtype=torch.bfloat16, device=q.device) if out is None else out
     n_sel = sel.shape[3]
-    ws = _block_ws(ws, L.mtp_block_sparse_attn_ws_bytes(cache.desc, B, T, nq, n_sel), q.device)
+    ws = _block_ws(cache, ws, L.mtp_block_sparse_attn_ws_bytes, (B, T, nq, n_sel), q.device)
     L.mtp_block_sparse_attn(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table,
                             block_table.shape[1], sel, n_sel,
                             1.0 / float(hd) ** 0.5 if scale is None else scale, out, out_lse, dev_err,

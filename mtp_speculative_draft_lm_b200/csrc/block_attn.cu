@@ -1096,7 +1096,8 @@ template <int HD, int NT, bool SPARSE>
 cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
     using Sh = Shape<HD, NT>;
     auto kern = block_attn_kernel<HD, NT, SPARSE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+    static std::atomic<uint64_t> devices{0};
+    cudaError_t e = allow_smem(kern, Sh::kSmem, devices);
     if (e != cudaSuccess) return e;
     int grid = sms * Sh::kPerSm;
     if (grid > kMaxGrid) grid = kMaxGrid;

@@ -5,6 +5,8 @@
 
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -168,6 +170,19 @@ __device__ __forceinline__ void pick_places(const uint32_t (&k)[KEYS], int n, ui
         if (in && (k[u] < thr || (k[u] == thr && eq < need))) *taken |= 1u << u;
         before[u] = (at & 0xffffu) + min(eq, need);
     }
+}
+
+// Lets `kern` use `bytes` of shared memory, asked for once per device.
+template <class K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& devices) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // Launches `kern` so that it may start while the kernel before it in the stream ends (each of
