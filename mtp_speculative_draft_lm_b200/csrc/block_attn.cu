@@ -255,6 +255,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     }
     // arrivals: lane 0 with the tiles' bytes, and one per tile for its scales
     if (tid < kWarps * ST) mbar_init(&full[tid], 1 + P);
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+    }
     if (tid == 0) *abort = 0;
     mbar_fence_init();
     __syncthreads();
@@ -760,124 +764,141 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             }
         }
 
+        const bool whole = t0 == 0 && t1 == sw.steps;
+        const bool more = next_unit(pl);  // (sw is the next unit's from here on)
+        if (more) load_q();               // (its rows arrive while this unit is joined)
+
         // join the four warps (fixed order): the largest reference M, everything times 2^(m - M)
-        float mr[NT][2], ls[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            mr[j][0] = (fresh >> (2 * j)) & 1u ? -INFINITY : -nm[j].x;
-            mr[j][1] = (fresh >> (2 * j + 1)) & 1u ? -INFINITY : -nm[j].y;
-            ls[j][0] = l[j].x, ls[j][1] = l[j].y;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l[j].x += __shfl_xor_sync(0xffffffffu, l[j].x, o);
+                l[j].y += __shfl_xor_sync(0xffffffffu, l[j].y, o);
+            }
+            if (gid == 0) {
+                const int r = warp * R + 8 * j + 2 * tig;
+                *reinterpret_cast<float2*>(redm + r) = make_float2((fresh >> (2 * j)) & 1u ? -INFINITY : -nm[j].x,
+                                                                  (fresh >> (2 * j + 1)) & 1u ? -INFINITY : -nm[j].y);
+                *reinterpret_cast<float2*>(redl + r) = l[j];
+            }
         }
+        __syncthreads();
+        float* slot = p.parts + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * (R * (HD + 4));
+        if (tid < R) {  // a thread per row: the warps' factors, the sum, and what does not need the accumulators
+            const int r = tid, tok = token_of(r), i = (row0 + r) - tok * p.group;
+            const int row = (b * (int)p.t.T + tok) * p.a.nq + g * p.group + i;
+            float m[kWarps], M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m[w] = redm[w * R + r]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) ls[j][e] += __shfl_xor_sync(0xffffffffu, ls[j][e], o);
-        if (gid == 0)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = warp * R + 8 * j + 2 * tig + e;
-                    redm[r] = mr[j][e];
-                    redl[r] = ls[j][e];
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = m[w] == -INFINITY ? 0.f : ex2(m[w] - M);
+                L += f * redl[w * R + r];
+                redm[w * R + r] = f;
+            }
+            const bool some = !(L <= 0.f);
+            redl[r] = whole ? (some ? 1.f / L : 0.f) : 1.f;
+            redl[R + r] = __int_as_float(row);
+            if (r < nrows) {
+                if (whole) {
+                    const float lse2 = some ? M + log2f(L) : -INFINITY;
+                    if (p.a.out_lse) p.a.out_lse[row] = lse2 * kLn2;
+                    if (!SPARSE && p.a.out_mass) p.row_lse[((int64_t)b * p.c.nkv + g) * mass_pitch + row0 + r] = lse2;
+                } else {
+                    slot[r] = M;
+                    slot[R + r] = L;
                 }
+            }
+        }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
+            const float2 f = *reinterpret_cast<const float2*>(redm + warp * R + 8 * j + 2 * tig);
+            const float f0 = f.x * vcur, f1 = f.y * vcur;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+                acc[dt][j][0] *= f0;
+                acc[dt][j][1] *= f1;
+                acc[dt][j][2] *= f0;
+                acc[dt][j][3] *= f1;
+            }
+        }
+        // each warp ends with a quarter of the columns: first halves are swapped between warps w and
+        // w ^ 2, then quarters between w and w ^ 1 (through the half that w has just read)
+        constexpr int H = DT / 2, Q = DT / 4;
+        float4* mine = xacc + (size_t)warp * H * NT * 32;
+        float4* other = xacc + (size_t)(warp ^ 2) * H * NT * 32;
+        float red[H][NT][4], fin[Q][NT][4];
+#pragma unroll
+        for (int dt = 0; dt < H; ++dt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float give[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    give[k] = warp & 2 ? acc[dt][j][k] : acc[H + dt][j][k];
+                    red[dt][j][k] = warp & 2 ? acc[H + dt][j][k] : acc[dt][j][k];
+                }
+                mine[(dt * NT + j) * 32 + lane] = make_float4(give[0], give[1], give[2], give[3]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int dt = 0; dt < H; ++dt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float4 v = other[(dt * NT + j) * 32 + lane];
+                red[dt][j][0] += v.x, red[dt][j][1] += v.y, red[dt][j][2] += v.z, red[dt][j][3] += v.w;
+            }
+#pragma unroll
+        for (int dt = 0; dt < Q; ++dt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float give[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    give[k] = warp & 1 ? red[dt][j][k] : red[Q + dt][j][k];
+                    fin[dt][j][k] = warp & 1 ? red[Q + dt][j][k] : red[dt][j][k];
+                }
+                other[(dt * NT + j) * 32 + lane] = make_float4(give[0], give[1], give[2], give[3]);
+            }
+        __syncthreads();
+        const float4* last = xacc + (size_t)(warp ^ 3) * H * NT * 32;
+        const int dt0 = warp * Q;  // (a half's quarters in order of the warps: 0, 1, then 2, 3)
+        const int col = (dt0 >> 3) * 128 + col_of<HD>(gid) + 2 * (dt0 & 7);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int dt = 0; dt < Q; ++dt) {
+                const float4 v = last[(dt * NT + j) * 32 + lane];
+                fin[dt][j][0] += v.x, fin[dt][j][1] += v.y, fin[dt][j][2] += v.z, fin[dt][j][3] += v.w;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * j + 2 * tig + e;
-                float M = redm[r];
+                if (r >= nrows) continue;
+                if (whole) {
+                    const float inv = redl[r];
+                    uint32_t o[Q];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) M = fmaxf(M, redm[w * R + r]);
-                const float mine = mr[j][e] == -INFINITY ? 0.f : ex2(mr[j][e] - M);
-                float L = 0.f;
+                    for (int dt = 0; dt < Q; ++dt)  // (a row without any weight has sums of 0, times 0)
+                        o[dt] = f32x2_to_bf16x2(fin[dt][j][e] * inv, fin[dt][j][2 + e] * inv);
+                    uint16_t* to = p.a.out + (int64_t)__float_as_int(redl[R + r]) * HD + col;
+                    if constexpr (Q == 1) *reinterpret_cast<uint32_t*>(to) = o[0];
+                    else if constexpr (Q == 2) *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
+                    else *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+                } else {
+                    float* to = slot + R * 4 + r * HD + col;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = redm[w * R + r] == -INFINITY ? 0.f : ex2(redm[w * R + r] - M);
-                    L += f * redl[w * R + r];
-                }
-                mr[j][e] = M;
-                ls[j][e] = L;
-                const float by = mine * vcur;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    acc[dt][j][e] *= by;
-                    acc[dt][j][2 + e] *= by;
-                }
-            }
-        // warps 2 and 3 hand theirs to 0 and 1, then 1 to 0
-#pragma unroll
-        for (int half = kWarps / 2; half; half >>= 1) {
-            if (warp >= half && warp < 2 * half) {
-                float4* to = xacc + (size_t)(half == 2 ? warp - half : 1) * DT * NT * 32;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        to[(dt * NT + j) * 32 + lane] = make_float4(acc[dt][j][0], acc[dt][j][1], acc[dt][j][2], acc[dt][j][3]);
-            }
-            __syncthreads();
-            if (warp < half) {
-                const float4* from = xacc + (size_t)(half == 2 ? warp : 1) * DT * NT * 32;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const float4 v = from[(dt * NT + j) * 32 + lane];
-                        acc[dt][j][0] += v.x;
-                        acc[dt][j][1] += v.y;
-                        acc[dt][j][2] += v.z;
-                        acc[dt][j][3] += v.w;
-                    }
-            }
-        }
-        if (warp == 0) {
-            const bool whole = t0 == 0 && t1 == sw.steps;
-            float* slot = p.parts + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * (R * (HD + 4));
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 8 * j + 2 * tig + e;
-                    if (r >= nrows) continue;
-                    const int tok = token_of(r), i = (row0 + r) - tok * p.group;
-                    const int64_t row = ((int64_t)b * p.t.T + tok) * p.a.nq + g * p.group + i;
-                    const bool some = !(ls[j][e] <= 0.f);
-                    const float inv = some ? 1.f / ls[j][e] : 0.f;
-#pragma unroll
-                    for (int dt = 0; dt < DT; dt += 4) {  // 8 columns
-                        const int d = (dt >> 3) * 128 + col_of<HD>(gid) + 2 * (dt & 7);
-                        if (whole) {
-                            uint32_t o4[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                o4[k] = some ? f32x2_to_bf16x2(acc[dt + k][j][e] * inv, acc[dt + k][j][2 + e] * inv) : 0u;
-                            *reinterpret_cast<uint4*>(p.a.out + row * HD + d) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; k += 2)
-                                *reinterpret_cast<float4*>(slot + R * 4 + r * HD + d + 2 * k) =
-                                    make_float4(acc[dt + k][j][e], acc[dt + k][j][2 + e], acc[dt + k + 1][j][e], acc[dt + k + 1][j][2 + e]);
-                        }
-                    }
-                    if (gid == 0) {
-                        if (whole) {
-                            const float lse2 = some ? mr[j][e] + log2f(ls[j][e]) : -INFINITY;
-                            if (p.a.out_lse) p.a.out_lse[row] = lse2 * kLn2;
-                            if (!SPARSE && p.a.out_mass) p.row_lse[((int64_t)b * p.c.nkv + g) * mass_pitch + row0 + r] = lse2;
-                        } else {
-                            slot[r] = mr[j][e];
-                            slot[R + r] = ls[j][e];
-                        }
+                    for (int dt = 0; dt < Q; dt += 2) {
+                        if constexpr (Q == 1) *reinterpret_cast<float2*>(to) = make_float2(fin[0][j][e], fin[0][j][2 + e]);
+                        else *reinterpret_cast<float4*>(to + 2 * dt) = make_float4(fin[dt][j][e], fin[dt][j][2 + e], fin[dt + 1][j][e], fin[dt + 1][j][2 + e]);
                     }
                 }
+            }
         }
         first = false;
-        if (!next_unit(pl)) break;
-        load_q();
+        if (!more) break;
     } while (true);
     // after a timeout: wait (again with a limit) for the copies that are still in flight
     if (*abort && lane == 0)
@@ -997,25 +1018,30 @@ __global__ void __launch_bounds__(32 * (WPR > 4 ? WPR : 4)) block_attn_join_kern
 }
 
 // out_mass[b, j] over a CTA's 32 tiles: a thread sums one tile's rows of every eighth kv head in
-// order, then the eight sums and the block's tiles are added in order.
+// order (they are neighbours: four at a time where T group allows), then the eight sums and the
+// block's tiles are added in order. (Lanes across the rows, one load in flight each, took 13
+// us where this takes 8.)
 __global__ void __launch_bounds__(256) block_mass_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float sums[8][32];
     const int b = blockIdx.y, t = threadIdx.x & 31, gs = threadIdx.x >> 5;
     const int tile = (int)blockIdx.x * 32 + t;
+    const SeqWork w = seq_work<1, false, 1>(p, b);  // (written before the kernels that let this one start)
+    const int pitch = (int)p.t.T * p.group, rows = w.q * p.group, rows4 = pitch % 4 ? 0 : rows & ~3;
     pdl_wait();
-    const SeqWork w = seq_work<1, false, 1>(p, b);
-    const int pitch = (int)p.t.T * p.group, rows = w.q * p.group;
     float sum = 0.f;
     if (tile < w.tiles)
         for (int g = gs; g < p.c.nkv; g += 8) {
             const int64_t head = (int64_t)b * p.c.nkv + g;
             const float* x = p.tile_lse + (head * p.tiles + tile) * pitch;
             const float* L = p.row_lse + head * pitch;
+            auto add = [&](float v, float l) { sum += v == -INFINITY ? 0.f : ex2(v - l); };
 #pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
-                const float v = x[r];
-                sum += v == -INFINITY ? 0.f : ex2(v - L[r]);
+            for (int r = 0; r < rows4; r += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(x + r), l = *reinterpret_cast<const float4*>(L + r);
+                add(v.x, l.x), add(v.y, l.y), add(v.z, l.z), add(v.w, l.w);
             }
+#pragma unroll 4
+            for (int r = rows4; r < rows; ++r) add(x[r], L[r]);
         }
     sums[gs][t] = sum;
     __syncthreads();
