@@ -254,6 +254,28 @@ def paged_decode_attn(q, nkv, k_cache, v_cache, block_table, seq_len, k_scale=1.
     return out, ws
 
 
+def _need(device: int, dtype, numel: int, *tensors):
+    """Raises unless each tensor (None: left out) is contiguous, of this type and size, on this device."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.numel() != numel or t.get_device() != device
+                              or not t.is_contiguous()):
+            raise ValueError(f"expected a contiguous {dtype} tensor of {numel} elements on device {device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _batch(cache: BlockCache, x, block_table, seq_lens, q_lens, dev_err) -> int:
+    """Checks a call's tokens x [B, ...] and the batch beside them; returns n_table."""
+    B, n_table = x.shape[0], block_table.shape[1]
+    dev = cache.device
+    if x.get_device() != dev or dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the cache is on device {dev}, the tokens on {x.get_device()}; both must be the current one")
+    _need(dev, torch.int32, B, seq_lens, q_lens)
+    _need(dev, torch.int32, B * n_table, block_table)
+    if dev_err is not None:
+        _need(dev, torch.int32, 1, dev_err)
+    return n_table
+
+
 @dataclass
 class BlockCache:
     """A block-scaled paged cache: E4M3 codes k, v with logical shape [num_blocks, nkv,
@@ -266,16 +288,18 @@ class BlockCache:
     k_mean: torch.Tensor | None = None
     k_mean_scale: torch.Tensor | None = None
     desc: L.mtp_block_cache = field(init=False)
+    device: int = field(init=False)
     ws_bytes: dict = field(init=False, default_factory=dict, repr=False)  # workspace sizes asked for
 
     def __post_init__(self):
         nb, nkv, bs, hd = self.k.shape
-        assert self.k.dtype == self.v.dtype == torch.uint8 and self.v.shape == self.k.shape
-        assert self.k.stride() == self.v.stride() and self.k.stride(3) == 1
-        for t in (self.k_scale, self.v_scale, self.k_mean_scale):
-            assert t is None or (t.shape == (nb, nkv) and t.dtype == torch.float32 and t.is_contiguous())
-        m = self.k_mean
-        assert m is None or (m.shape == (nb, nkv, hd) and m.dtype == torch.int8 and m.is_contiguous())
+        self.device = self.k.get_device()
+        if self.k.dtype is not torch.uint8 or self.v.dtype is not torch.uint8 or self.v.shape != self.k.shape:
+            raise ValueError("k and v: uint8 codes of one shape")
+        if self.k.stride() != self.v.stride() or self.k.stride(3) != 1 or self.v.get_device() != self.device:
+            raise ValueError("k and v: one layout with hd contiguous, on one device")
+        _need(self.device, torch.float32, nb * nkv, self.k_scale, self.v_scale, self.k_mean_scale)
+        _need(self.device, torch.int8, nb * nkv * hd, self.k_mean)
         self.desc = L.mtp_block_cache(nkv, hd, bs, 0, nb, self.k.stride(0), self.k.stride(1),
                                       self.k.stride(2), *(L._ptr(t) for t in (
                                           self.k, self.v, self.k_scale, self.v_scale, self.k_mean,
@@ -318,12 +342,24 @@ def _token_stride(x: torch.Tensor) -> int:
     return step
 
 
-def _block_ws(cache: BlockCache, ws, size, key: tuple, device):
+def _new(shape, dtype, device: int, stream):
+    """A tensor for a call on `stream` (None: the current one)."""
+    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
+    if isinstance(stream, torch.cuda.Stream):
+        t.record_stream(stream)
+    return t
+
+
+def _block_ws(cache: BlockCache, ws, size, key: tuple, stream):
     """ws if it is large enough, else a new one; size(desc, *key) says how large (asked once per key)."""
     nbytes = cache.ws_bytes.get((size, key))
     if nbytes is None:
         nbytes = cache.ws_bytes[size, key] = size(cache.desc, *key)
-    return torch.empty((nbytes,), dtype=torch.uint8, device=device) if ws is None or ws.numel() < nbytes else ws
+    if ws is None or ws.nbytes < nbytes:
+        return _new((nbytes,), torch.uint8, cache.device, stream)
+    if ws.get_device() != cache.device or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous on the cache's device")
+    return ws
 
 
 def block_append(cache: BlockCache, k, v, block_table, seq_lens, q_lens=None, dev_err=None,
@@ -332,23 +368,34 @@ def block_append(cache: BlockCache, k, v, block_table, seq_lens, q_lens=None, de
     of each sequence (seq_lens counts them already) and updates scales and means."""
     B, T, n, hd = k.shape
     step, d = _token_stride(k), cache.desc
-    if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride() or n != d.nkv or hd != d.hd:
-        raise ValueError("k and v must be the cache's heads with one stride")
-    L.mtp_block_append(d, k, v, step, B, T, seq_lens, q_lens, block_table,
-                       block_table.shape[1], dev_err, stream)
+    if (v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride() or n != d.nkv or hd != d.hd
+            or v.get_device() != cache.device):
+        raise ValueError("k and v must be the cache's heads with one stride, on its device")
+    n_table = _batch(cache, k, block_table, seq_lens, q_lens, dev_err)
+    L.mtp_block_append(d, k, v, step, B, T, seq_lens, q_lens, block_table, n_table, dev_err, stream)
+
+
+def _queries(cache: BlockCache, q, block_table, seq_lens, q_lens, dev_err):
+    B, T, nq, hd = q.shape
+    if hd != cache.desc.hd:
+        raise ValueError(f"q has heads of {hd}, the cache of {cache.desc.hd}")
+    return B, T, nq, _token_stride(q), _batch(cache, q, block_table, seq_lens, q_lens, dev_err)
 
 
 def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=None, out=None,
                out_lse=None, mass=None, out_mass=None, ws=None, dev_err=None, stream=None):
     """Attention of q [B, T, nq, hd] over each sequence's cached positions (causal among the T
-    tokens); out_mass accumulates each block's softmax weight. Returns (out, ws)."""
-    B, T, nq, hd = q.shape
-    out = torch.empty((B, T, nq, hd), dtype=torch.bfloat16, device=q.device) if out is None else out
-    n_table = block_table.shape[1]
-    ws = _block_ws(cache, ws, L.mtp_block_attn_ws_bytes, (B, T, nq, n_table, out_mass is not None), q.device)
-    L.mtp_block_attn(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table, n_table,
-                     1.0 / float(hd) ** 0.5 if scale is None else scale, out, out_lse, mass, out_mass,
-                     dev_err, ws, ws.numel(), stream)
+    tokens); out_mass [B, n_table] accumulates each block's softmax weight. Returns (out, ws); a
+    ws that is passed in again saves its allocation."""
+    B, T, nq, step, n_table = _queries(cache, q, block_table, seq_lens, q_lens, dev_err)
+    out = _new(q.shape, torch.bfloat16, cache.device, stream) if out is None else out
+    _need(cache.device, torch.bfloat16, q.numel(), out)
+    _need(cache.device, torch.float32, B * T * nq, out_lse)
+    _need(cache.device, torch.float32, B * n_table, mass, out_mass)
+    ws = _block_ws(cache, ws, L.mtp_block_attn_ws_bytes, (B, T, nq, n_table, out_mass is not None), stream)
+    L.mtp_block_attn(cache.desc, q, step, B, T, nq, seq_lens, q_lens, block_table, n_table,
+                     cache.desc.hd ** -0.5 if scale is None else scale, out, out_lse, mass, out_mass,
+                     dev_err, ws, ws.nbytes, stream)
     return out, ws
 
 
@@ -356,26 +403,29 @@ def block_select(cache: BlockCache, q, block_table, seq_lens, n_sel, n_first=1, 
                  q_lens=None, out=None, ws=None, dev_err=None, stream=None):
     """The n_sel blocks that each token and kv head attends to, by the 8-bit product of its
     query heads with the blocks' mean keys: (sel [B, T, nkv, n_sel] i32, ws)."""
-    B, T, nq, _ = q.shape
-    n_table = block_table.shape[1]
-    out = torch.empty((B, T, cache.desc.nkv, n_sel), dtype=torch.int32, device=q.device) if out is None else out
-    ws = _block_ws(cache, ws, L.mtp_block_select_ws_bytes, (B, T, n_table), q.device)
-    L.mtp_block_select(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table, n_table,
-                       n_sel, n_first, n_last, out, dev_err, ws, ws.numel(), stream)
+    B, T, nq, step, n_table = _queries(cache, q, block_table, seq_lens, q_lens, dev_err)
+    nkv = cache.desc.nkv
+    out = _new((B, T, nkv, n_sel), torch.int32, cache.device, stream) if out is None else out
+    _need(cache.device, torch.int32, B * T * nkv * n_sel, out)
+    ws = _block_ws(cache, ws, L.mtp_block_select_ws_bytes, (B, T, n_table), stream)
+    L.mtp_block_select(cache.desc, q, step, B, T, nq, seq_lens, q_lens, block_table, n_table, n_sel,
+                       n_first, n_last, out, dev_err, ws, ws.nbytes, stream)
     return out, ws
 
 
 def block_sparse_attn(cache: BlockCache, q, block_table, seq_lens, sel, q_lens=None, scale=None,
                       out=None, out_lse=None, ws=None, dev_err=None, stream=None):
     """block_attn over the blocks that sel [B, T, nkv, n_sel] lists. Returns (out, ws)."""
-    B, T, nq, hd = q.shape
-    out = torch.empty((B, T, nq, hd), dtype=torch.bfloat16, device=q.device) if out is None else out
+    B, T, nq, step, n_table = _queries(cache, q, block_table, seq_lens, q_lens, dev_err)
     n_sel = sel.shape[3]
-    ws = _block_ws(cache, ws, L.mtp_block_sparse_attn_ws_bytes, (B, T, nq, n_sel), q.device)
-    L.mtp_block_sparse_attn(cache.desc, q, _token_stride(q), B, T, nq, seq_lens, q_lens, block_table,
-                            block_table.shape[1], sel, n_sel,
-                            1.0 / float(hd) ** 0.5 if scale is None else scale, out, out_lse, dev_err,
-                            ws, ws.numel(), stream)
+    _need(cache.device, torch.int32, B * T * cache.desc.nkv * n_sel, sel)
+    out = _new(q.shape, torch.bfloat16, cache.device, stream) if out is None else out
+    _need(cache.device, torch.bfloat16, q.numel(), out)
+    _need(cache.device, torch.float32, B * T * nq, out_lse)
+    ws = _block_ws(cache, ws, L.mtp_block_sparse_attn_ws_bytes, (B, T, nq, n_sel), stream)
+    L.mtp_block_sparse_attn(cache.desc, q, step, B, T, nq, seq_lens, q_lens, block_table, n_table, sel,
+                            n_sel, cache.desc.hd ** -0.5 if scale is None else scale, out, out_lse,
+                            dev_err, ws, ws.nbytes, stream)
     return out, ws
 
 
@@ -384,10 +434,17 @@ def block_evict(block_table, seq_lens, mass, block_size, keep, n_first=1, n_last
     """Bounds each sequence to `keep` blocks by accumulated weight: (out_table, out_lens,
     out_mass, freed, n_freed). Outputs may be the inputs (in place)."""
     B, n_table = block_table.shape
-    new = lambda t, like: torch.empty_like(like) if t is None else t  # noqa: E731
-    out_table, freed = new(out_table, block_table), new(freed, block_table)
-    out_lens, n_freed = new(out_lens, seq_lens), new(n_freed, seq_lens)
-    out_mass = new(out_mass, mass)
+    dev = block_table.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"block_table is on device {dev}, which must be the current one")
+    out_table = _new((B, n_table), torch.int32, dev, stream) if out_table is None else out_table
+    freed = _new((B, n_table), torch.int32, dev, stream) if freed is None else freed
+    out_lens = _new((B,), torch.int32, dev, stream) if out_lens is None else out_lens
+    n_freed = _new((B,), torch.int32, dev, stream) if n_freed is None else n_freed
+    out_mass = _new((B, n_table), torch.float32, dev, stream) if out_mass is None else out_mass
+    _need(dev, torch.int32, B * n_table, block_table, out_table, freed)
+    _need(dev, torch.int32, B, seq_lens, out_lens, n_freed)
+    _need(dev, torch.float32, B * n_table, mass, out_mass)
     L.mtp_block_evict(B, block_table, n_table, seq_lens, mass, block_size, keep, n_first, n_last,
                       out_table, out_lens, out_mass, freed, n_freed, stream)
     return out_table, out_lens, out_mass, freed, n_freed

@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(32 * (WPR > 4 ? WPR : 4)) block_attn_join_kern
     }
     // (the lengths were written before the kernel that lets this one start)
     const SeqWork sw = seq_work<NT, SPARSE, P>(p, b);
-    const int g = (int)(((uint32_t)head * p.group_inv) >> 20);
+    const int g = head / p.group;
     const int r_abs = SPARSE ? head - g * p.group : tok * p.group + head - g * p.group;
     const int part = SPARSE ? tok : r_abs / R, r = SPARSE ? r_abs : r_abs - part * R;
     pdl_wait();
