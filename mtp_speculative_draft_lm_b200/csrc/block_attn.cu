@@ -13,8 +13,8 @@
 //
 // Work: the cache is read in tiles of 16 positions, each inside one block. A unit is a kv head
 // of a sequence with up to 8 NT of its T (nq / nkv) query rows (for listed blocks: of a
-// token). All units' tiles form one line; each CTA takes an equal stretch of it, however
-// ragged the batch. A unit that lies in one CTA is finished there; the others' partial sums go
+// token). All units form one line, each as long as its steps and kUnitCost more, and each CTA
+// takes an equal stretch of it, however ragged the batch. A unit that lies in one CTA is finished there; the others' partial sums go
 // to the workspace and a second kernel joins them in order of the CTAs (fixed order: the same
 // bits every time).
 //
@@ -45,6 +45,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxGrid = 640;                  // CTAs (workspace slots are sized for it)
+// Steps of the line before each unit's first: what its rows, joins and barriers cost (3 us against
+// half a microsecond a step). A verify batch with short sequences took 56 us with none: the CTAs that
+// had the short ones were the last by a third of that (44 us with 12 or 16, 45 with 8, 48 with 32).
+constexpr int kUnitCost = 12;
 constexpr float kRaise = 8.f;                  // binades a score may exceed the reference by
 
 struct AttnParams {
@@ -55,7 +59,7 @@ struct AttnParams {
     int row_tiles;       // dense: row tiles of 8 NT rows that T tokens have at most
     int64_t tiles;       // 16-position tiles of n_table blocks (tile_lse's pitch)
     int32_t* per;        // [1] steps per CTA
-    int32_t* unit_base;  // [units] first step of each unit on the line
+    int32_t* unit_base;  // [units] where each unit starts on the line
     int tile_shift;      // log2(16-position tiles per block)
     uint32_t group_inv;  // ceil(2^20 / group): r / group = r group_inv >> 20 for r <= 1024
     float* parts;        // [2 kMaxGrid][8 NT (hd + 4)] partial sums of a CTA's first and last unit
@@ -68,6 +72,7 @@ struct AttnParams {
 // tiles and steps of `P` tiles that each has.
 struct SeqWork {
     int len, q, outer, inner, tiles, steps;
+    __device__ __forceinline__ int line() const { return steps ? outer * inner * (steps + kUnitCost) : 0; }
 };
 template <int NT, bool SPARSE, int P>
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
@@ -265,14 +270,13 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     pdl_wait();  // everything below reads or writes memory that earlier kernels may still use
     pdl_launch_dependents();  // (the next kernel may read what was there before this one)
 
-    // this CTA's stretch of the line: `stretch` steps from `beg` on, and the sequence, unit and
-    // step it starts with (every warp for itself, 32 sequences at a time)
+    // this CTA's stretch of the line: `stretch` from `beg` on, and the sequence and unit it
+    // starts with (every warp for itself, 32 sequences at a time)
     const int B = p.t.B;
     SeqWork w0 = seq_work<NT, SPARSE, P>(p, min(lane, B - 1));
-    int n0 = lane < B ? w0.outer * w0.inner * w0.steps : 0, total = n0;
+    int n0 = lane < B ? w0.line() : 0, total = n0;
     for (int b = 32 + lane; b < B; b += 32) {
-        const SeqWork w = seq_work<NT, SPARSE, P>(p, b);
-        total += w.outer * w.inner * w.steps;
+        total += seq_work<NT, SPARSE, P>(p, b).line();
     }
     total = __reduce_add_sync(0xffffffffu, total);
     const int grid = (int)gridDim.x;
@@ -282,17 +286,18 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
     const int beg = (int)blockIdx.x * per;
     const int stretch = min(total - beg, per);
 
-    // A place on the line: a unit and the steps [t0, t1) of it that belong to this CTA.
+    // A place on the line: a unit, where in it the stretch enters, and the steps [t0, t1) of it
+    // that belong to this CTA.
     struct Place {
         SeqWork sw;
-        int b, outer, inner, t0, t1;
-        int left;  // steps of the stretch from t0 on
+        int b, outer, inner, off, t0, t1;
+        int left;  // of the stretch, from there on
     };
     Place pl;
     for (int b0 = 0, before = 0;; b0 += 32) {
         if (b0) {
             w0 = seq_work<NT, SPARSE, P>(p, min(b0 + lane, B - 1));
-            n0 = b0 + lane < B ? w0.outer * w0.inner * w0.steps : 0;
+            n0 = b0 + lane < B ? w0.line() : 0;
         }
         int inc = n0;
 #pragma unroll
@@ -311,31 +316,38 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
             pl.sw.tiles = __shfl_sync(0xffffffffu, w0.tiles, src);
             pl.sw.steps = __shfl_sync(0xffffffffu, w0.steps, src);
             pl.b = b0 + src;
-            const int u = off / pl.sw.steps;
-            pl.t0 = off - u * pl.sw.steps;
+            const int u = off / (pl.sw.steps + kUnitCost);
+            pl.off = off - u * (pl.sw.steps + kUnitCost);
             pl.outer = u / pl.sw.inner;
             pl.inner = u - pl.outer * pl.sw.inner;
             break;
         }
         before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    pl.left = stretch;
-    pl.t1 = min(pl.sw.steps, pl.t0 + pl.left);
-    auto next_unit = [&](Place& c) -> bool {  // false at the stretch's end
-        c.left -= c.t1 - c.t0;
-        if (c.left <= 0) return false;
-        c.t0 = 0;
-        if (++c.inner == c.sw.inner) {
-            c.inner = 0;
-            if (++c.outer == c.sw.outer) {
-                c.outer = 0;
-                do c.sw = seq_work<NT, SPARSE, P>(p, ++c.b);
-                while (c.sw.outer * c.sw.inner * c.sw.steps == 0 && c.b + 1 < B);
+    auto settle = [&](Place& c) {
+        c.t0 = max(c.off - kUnitCost, 0);
+        c.t1 = min(max(c.off + c.left - kUnitCost, 0), c.sw.steps);
+    };
+    auto next_unit = [&](Place& c) -> bool {  // the next one with a step; false at the stretch's end
+        do {
+            c.left -= c.sw.steps + kUnitCost - c.off;
+            if (c.left <= 0) return false;
+            c.off = 0;
+            if (++c.inner == c.sw.inner) {
+                c.inner = 0;
+                if (++c.outer == c.sw.outer) {
+                    c.outer = 0;
+                    do c.sw = seq_work<NT, SPARSE, P>(p, ++c.b);
+                    while (c.sw.line() == 0 && c.b + 1 < B);
+                }
             }
-        }
-        c.t1 = min(c.sw.steps, c.left);
+            settle(c);
+        } while (c.t0 == c.t1);
         return true;
     };
+    pl.left = stretch;
+    settle(pl);
+    if (pl.t0 == pl.t1 && !next_unit(pl)) return;
 
     // The copies' side of this warp, ST steps ahead. Lane l looks up tile l % P of the warp's
     // step l / P from ah_step on; ah_n counts the steps of those that have been issued.
@@ -449,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         if (tid == 0) {
             if (!SPARSE && t1 == sw.steps && (sw.len - 1) / p.c.bs >= p.t.n_table)
                 raise_flag(p.t.dev_err, DEVFLAG_BAD_SLOT);  // positions past the table
-            if (t0 == 0) p.unit_base[unit_index<SPARSE>(p, b, g, part)] = beg + (stretch - pl.left);
+            if (t0 == 0) p.unit_base[unit_index<SPARSE>(p, b, g, part)] = beg + (stretch - pl.left) - pl.off;
         }
 
         __syncthreads();  // the previous unit's rows and sums are no longer needed
@@ -526,29 +538,40 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 // scores of 16 positions (rows) and the unit's query rows (columns)
 #pragma unroll
                 for (int h = 0; h < HD / 64; ++h) {  // 64 dims at a time
+                    uint32_t w0[HJ][4], w1[HJ][4];
 #pragma unroll
                     for (int z = 0; z < HJ; ++z) {
                         const uint32_t ka = (stage + z * 2 * S::kTile + (h >> 1) * 2048 + koff) ^ ((h & 1) << 6);
                         const uint4 k0 = lds4(ka), k1 = lds4(ka + 8 * kPitch);
-                        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+                        w0[z][0] = k0.x, w0[z][1] = k0.y, w0[z][2] = k0.z, w0[z][3] = k0.w;
+                        w1[z][0] = k1.x, w1[z][1] = k1.y, w1[z][2] = k1.z, w1[z][3] = k1.w;
+                    }
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            uint32_t a[2][4];
+                    for (int t = 0; t < 2; ++t) {
+                        uint32_t a[HJ][2][4];
+#pragma unroll
+                        for (int z = 0; z < HJ; ++z)
 #pragma unroll
                             for (int v = 0; v < 2; ++v) {
-                                a[v][0] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] & 0xFFFFu));
-                                a[v][1] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] & 0xFFFFu));
-                                a[v][2] = e4m3x2_to_f16x2((uint16_t)(w0[2 * t + v] >> 16));
-                                a[v][3] = e4m3x2_to_f16x2((uint16_t)(w1[2 * t + v] >> 16));
+                                a[z][v][0] = e4m3x2_to_f16x2((uint16_t)(w0[z][2 * t + v] & 0xFFFFu));
+                                a[z][v][1] = e4m3x2_to_f16x2((uint16_t)(w1[z][2 * t + v] & 0xFFFFu));
+                                a[z][v][2] = e4m3x2_to_f16x2((uint16_t)(w0[z][2 * t + v] >> 16));
+                                a[z][v][3] = e4m3x2_to_f16x2((uint16_t)(w1[z][2 * t + v] >> 16));
                             }
+                        uint4 q4[NT];
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                const uint4 q4 = NT == 1 ? qf[2 * h + t] : *reinterpret_cast<const uint4*>(qh + (8 * j + gid) * QP + 64 * h + 16 * tig + 8 * t);
-                                if (h == 0 && t == 0) mma_f16_first(x[z][j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
-                                else mma_f16_16816(x[z][j], a[0][0], a[0][1], a[0][2], a[0][3], q4.x, q4.y);
-                                mma_f16_16816(x[z][j], a[1][0], a[1][1], a[1][2], a[1][3], q4.z, q4.w);
-                            }
-                        }
+                        for (int j = 0; j < NT; ++j)
+                            q4[j] = NT == 1 ? qf[2 * h + t] : *reinterpret_cast<const uint4*>(qh + (8 * j + gid) * QP + 64 * h + 16 * tig + 8 * t);
+                        // (products onto one sum as far apart as they can be)
+#pragma unroll
+                        for (int v = 0; v < 2; ++v)
+#pragma unroll
+                            for (int z = 0; z < HJ; ++z)
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) {
+                                    if (h == 0 && t == 0 && v == 0) mma_f16_first(x[z][j], a[z][v][0], a[z][v][1], a[z][v][2], a[z][v][3], q4[j].x, q4[j].y);
+                                    else mma_f16_16816(x[z][j], a[z][v][0], a[z][v][1], a[z][v][2], a[z][v][3], v ? q4[j].z : q4[j].x, v ? q4[j].w : q4[j].y);
+                                }
                     }
                 }
                 // s - m, (row 2 tig, row 2 tig + 1) of positions gid and gid + 8; masked ones -inf
@@ -933,11 +956,11 @@ __global__ void __launch_bounds__(32 * (WPR > 4 ? WPR : 4)) block_attn_join_kern
     for (int v = 0; v < V; ++v) a[v] = 0.f;
     if (sw.steps > 0) {
         const int per = *p.per, base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
-        const int c0 = base / per, c1 = (base + sw.steps - 1) / per;
+        const int c0 = (base + kUnitCost) / per, c1 = (base + kUnitCost + sw.steps - 1) / per;  // of its first and last step
         if (c0 == c1) return;  // finished by one CTA
         // in CTA c0 the unit is the last (slot 1) unless it is also the first; in later ones the first
         auto slot = [&](int c) {
-            return p.parts + (int64_t)(c * 2 + (c == c0 && base != c0 * per ? 1 : 0)) * (R * (HD + 4));
+            return p.parts + (int64_t)(c * 2 + (c == c0 && c0 * per < base ? 1 : 0)) * (R * (HD + 4));
         };
         for (int k0 = c0 + wr; k0 <= c1; k0 += K * WPR) {
             float m[K], l[K], x[K][V];
@@ -1167,7 +1190,7 @@ cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const Bl
     if ((int64_t)t.B * t.T * a.nq > INT32_MAX) return cudaErrorInvalidValue;
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     // tiles of all units on one line: 32-bit indices
-    if ((double)l.units * (double)(sparse ? (int64_t)a.n_sel * (c.bs / 16) : l.tiles) >= 2147483648.0) return cudaErrorInvalidValue;
+    if ((double)l.units * (double)((sparse ? (int64_t)a.n_sel * (c.bs / 16) : l.tiles) + kUnitCost) >= 2147483648.0) return cudaErrorInvalidValue;
     AttnParams p{c, t, a, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int32_t*>(ws),
                  reinterpret_cast<int32_t*>(ws + l.base), c.bs == 16 ? 0 : c.bs == 32 ? 1 : 2,
                  ((1u << 20) + (uint32_t)(a.nq / c.nkv) - 1u) / (uint32_t)(a.nq / c.nkv), reinterpret_cast<float*>(ws + l.parts),
