@@ -55,6 +55,7 @@ struct AttnParams {
     BlockCache c;
     BlockBatch t;
     BlockAttnArgs a;
+    int grid;            // CTAs of block_attn_kernel
     int group;
     int row_tiles;       // dense: row tiles of 8 NT rows that T tokens have at most
     int64_t tiles;       // 16-position tiles of n_table blocks (tile_lse's pitch)
@@ -91,6 +92,11 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
     }
     w.steps = (w.tiles + P - 1) / P;
     return w;
+}
+
+// What each of `grid` CTAs takes of a line of this length.
+__device__ __forceinline__ int stretch_of(int total, int grid) {
+    return (total / grid + (total % grid != 0) + kWarps - 1) / kWarps * kWarps;
 }
 
 // The unit's index in unit_base: unit u of sequence b.
@@ -279,8 +285,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
         total += seq_work<NT, SPARSE, P>(p, b).line();
     }
     total = __reduce_add_sync(0xffffffffu, total);
-    const int grid = (int)gridDim.x;
-    const int per = (total / grid + (total % grid != 0) + kWarps - 1) / kWarps * kWarps;
+    const int per = stretch_of(total, p.grid);
     if (blockIdx.x == 0 && tid == 0) *p.per = per;
     if ((int64_t)blockIdx.x * per >= total) return;
     const int beg = (int)blockIdx.x * per;
@@ -949,13 +954,22 @@ __global__ void __launch_bounds__(32 * (WPR > 4 ? WPR : 4)) block_attn_join_kern
     const int g = head / p.group;
     const int r_abs = SPARSE ? head - g * p.group : tok * p.group + head - g * p.group;
     const int part = SPARSE ? tok : r_abs / R, r = SPARSE ? r_abs : r_abs - part * R;
+    int per = 0, base = 0;  // the CTAs' stretch, and where the row's unit starts on the line
+    if (p.t.B <= 32) {      // found while the parts are still being summed
+        const int n = lane < p.t.B ? seq_work<NT, SPARSE, P>(p, min(lane, p.t.B - 1)).line() : 0;
+        per = stretch_of(__reduce_add_sync(0xffffffffu, n), p.grid);
+        base = __reduce_add_sync(0xffffffffu, lane < b ? n : 0) + (SPARSE ? part * p.c.nkv + g : g * sw.inner + part) * (sw.steps + kUnitCost);
+    }
     pdl_wait();
     if (tok >= sw.q) return;
     float M = -INFINITY, L = 0.f, a[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a[v] = 0.f;
     if (sw.steps > 0) {
-        const int per = *p.per, base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
+        if (p.t.B > 32) {
+            per = *p.per;
+            base = p.unit_base[unit_index<SPARSE>(p, b, g, part)];
+        }
         const int c0 = (base + kUnitCost) / per, c1 = (base + kUnitCost + sw.steps - 1) / per;  // of its first and last step
         if (c0 == c1) return;  // finished by one CTA
         // in CTA c0 the unit is the last (slot 1) unless it is also the first; in later ones the first
@@ -1142,7 +1156,7 @@ bool cache_map(CUtensorMap* m, const BlockCache& c, const uint8_t* base) {
 }
 
 template <int HD, int NT, bool SPARSE>
-cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
+cudaError_t launch_attn(AttnParams p, const CUtensorMap& km, const CUtensorMap& vm, int sms, cudaStream_t s) {
     using Sh = Shape<HD, NT>;
     auto kern = block_attn_kernel<HD, NT, SPARSE>;
     static std::atomic<uint64_t> devices{0};
@@ -1150,6 +1164,7 @@ cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& km, const CUtens
     if (e != cudaSuccess) return e;
     int grid = sms * Sh::kPerSm;
     if (grid > kMaxGrid) grid = kMaxGrid;
+    p.grid = grid;
     if ((e = launch_after(kern, dim3((unsigned)grid), kThreads, Sh::kSmem, s, p, km, vm)) != cudaSuccess) return e;
     // eight warps per row while the rows are few (many parts each), one when they fill the GPU
     const int64_t rows = (int64_t)p.t.B * p.t.T * p.a.nq;
@@ -1191,7 +1206,7 @@ cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const Bl
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     // tiles of all units on one line: 32-bit indices
     if ((double)l.units * (double)((sparse ? (int64_t)a.n_sel * (c.bs / 16) : l.tiles) + kUnitCost) >= 2147483648.0) return cudaErrorInvalidValue;
-    AttnParams p{c, t, a, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int32_t*>(ws),
+    AttnParams p{c, t, a, 0, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int32_t*>(ws),
                  reinterpret_cast<int32_t*>(ws + l.base), c.bs == 16 ? 0 : c.bs == 32 ? 1 : 2,
                  ((1u << 20) + (uint32_t)(a.nq / c.nkv) - 1u) / (uint32_t)(a.nq / c.nkv), reinterpret_cast<float*>(ws + l.parts),
                  reinterpret_cast<float*>(ws + l.row_lse), reinterpret_cast<float*>(ws + l.tile_lse)};
