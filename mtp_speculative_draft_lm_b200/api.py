@@ -3,6 +3,7 @@
 No arithmetic of the method happens in Python."""
 from __future__ import annotations
 
+import ctypes as C
 from dataclasses import dataclass, field
 
 import torch
@@ -263,19 +264,6 @@ def _need(device: int, dtype, numel: int, *tensors):
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _batch(cache: BlockCache, x, block_table, seq_lens, q_lens, dev_err) -> int:
-    """Checks a call's tokens x [B, ...] and the batch beside them; returns n_table."""
-    B, n_table = x.shape[0], block_table.shape[1]
-    dev = cache.device
-    if x.get_device() != dev or dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"the cache is on device {dev}, the tokens on {x.get_device()}; both must be the current one")
-    _need(dev, torch.int32, B, seq_lens, q_lens)
-    _need(dev, torch.int32, B * n_table, block_table)
-    if dev_err is not None:
-        _need(dev, torch.int32, 1, dev_err)
-    return n_table
-
-
 @dataclass
 class BlockCache:
     """A block-scaled paged cache: E4M3 codes k, v with logical shape [num_blocks, nkv,
@@ -289,7 +277,6 @@ class BlockCache:
     k_mean_scale: torch.Tensor | None = None
     desc: L.mtp_block_cache = field(init=False)
     device: int = field(init=False)
-    ws_bytes: dict = field(init=False, default_factory=dict, repr=False)  # workspace sizes asked for
 
     def __post_init__(self):
         nb, nkv, bs, hd = self.k.shape
@@ -330,56 +317,64 @@ class BlockCache:
                    torch.full_like(ks, float(v_scale)))
 
 
+_calls = None
+
+
+def _block():
+    """The module that makes the block cache's calls (csrc/block_calls.cpp), with the library's
+    functions. It checks each tensor (type, size, contiguity, device) before the call."""
+    global _calls
+    if _calls is None:
+        lib = L.load()
+        from . import _block as m
+
+        m.init(*(C.cast(getattr(lib, n), C.c_void_p).value for n in (
+            "mtp_block_append", "mtp_block_attn_ws_bytes", "mtp_block_attn",
+            "mtp_block_select_ws_bytes", "mtp_block_select", "mtp_block_sparse_attn_ws_bytes",
+            "mtp_block_sparse_attn", "mtp_block_evict")))
+        _calls = m
+    return _calls
+
+
 def _token_stride(x: torch.Tensor) -> int:
     """Elements between the tokens of x [B, T, heads, hd], whose heads are packed."""
-    B, T, n, hd = x.shape
-    st = x.stride()
-    if x.dtype is not torch.bfloat16 or st[3] != 1 or (n > 1 and st[2] != hd):
-        raise ValueError("expected bf16 [B, T, heads, hd] with packed heads")
-    step = st[1] if T > 1 else st[0] if B > 1 else n * hd
-    if B > 1 and st[0] != T * step:
-        raise ValueError("sequences must be T token strides apart")
-    return step
+    return _block().token_stride(x)
 
 
 def _new(shape, dtype, device: int, stream):
     """A tensor for a call on `stream` (None: the current one)."""
+    if device < 0:
+        raise ValueError("the tensors must be on a GPU")
     t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
     if isinstance(stream, torch.cuda.Stream):
         t.record_stream(stream)
     return t
 
 
-def _block_ws(cache: BlockCache, ws, size, key: tuple, stream):
-    """ws if it is large enough, else a new one; size(desc, *key) says how large (asked once per key)."""
-    nbytes = cache.ws_bytes.get((size, key))
-    if nbytes is None:
-        nbytes = cache.ws_bytes[size, key] = size(cache.desc, *key)
-    if ws is None or ws.nbytes < nbytes:
-        return _new((nbytes,), torch.uint8, cache.device, stream)
-    if ws.get_device() != cache.device or not ws.is_contiguous():
-        raise ValueError("ws must be contiguous on the cache's device")
+def _with_ws(where: str, call, head: tuple, tail: tuple, ws, device: int, stream):
+    """Makes a call whose last argument is its workspace, with a new one if ws is None or too
+    small (the call then says how large, and launches nothing); returns the workspace."""
+    r = call(*head, *tail, ws)
+    if r > 0:
+        ws = _new((r,), torch.uint8, device, stream)
+        r = call(*head, *tail, ws)
+    if r:
+        raise L.MtpError(-r, where)
     return ws
+
+
+def _head(cache: BlockCache, x, block_table, seq_lens, q_lens, dev_err, stream) -> tuple:
+    return (C.addressof(cache.desc), cache.device, x, block_table, seq_lens, q_lens, dev_err,
+            L._stream(stream))
 
 
 def block_append(cache: BlockCache, k, v, block_table, seq_lens, q_lens=None, dev_err=None,
                  stream=None):
     """Writes the new rows k, v [B, T, nkv, hd] (bf16, slices of a projection allowed) at the end
     of each sequence (seq_lens counts them already) and updates scales and means."""
-    B, T, n, hd = k.shape
-    step, d = _token_stride(k), cache.desc
-    if (v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride() or n != d.nkv or hd != d.hd
-            or v.get_device() != cache.device):
-        raise ValueError("k and v must be the cache's heads with one stride, on its device")
-    n_table = _batch(cache, k, block_table, seq_lens, q_lens, dev_err)
-    L.mtp_block_append(d, k, v, step, B, T, seq_lens, q_lens, block_table, n_table, dev_err, stream)
-
-
-def _queries(cache: BlockCache, q, block_table, seq_lens, q_lens, dev_err):
-    B, T, nq, hd = q.shape
-    if hd != cache.desc.hd:
-        raise ValueError(f"q has heads of {hd}, the cache of {cache.desc.hd}")
-    return B, T, nq, _token_stride(q), _batch(cache, q, block_table, seq_lens, q_lens, dev_err)
+    r = _block().append(*_head(cache, k, block_table, seq_lens, q_lens, dev_err, stream), v)
+    if r:
+        raise L.MtpError(-r, "mtp_block_append")
 
 
 def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=None, out=None,
@@ -387,15 +382,10 @@ def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=N
     """Attention of q [B, T, nq, hd] over each sequence's cached positions (causal among the T
     tokens); out_mass [B, n_table] accumulates each block's softmax weight. Returns (out, ws); a
     ws that is passed in again saves its allocation."""
-    B, T, nq, step, n_table = _queries(cache, q, block_table, seq_lens, q_lens, dev_err)
     out = _new(q.shape, torch.bfloat16, cache.device, stream) if out is None else out
-    _need(cache.device, torch.bfloat16, q.numel(), out)
-    _need(cache.device, torch.float32, B * T * nq, out_lse)
-    _need(cache.device, torch.float32, B * n_table, mass, out_mass)
-    ws = _block_ws(cache, ws, L.mtp_block_attn_ws_bytes, (B, T, nq, n_table, out_mass is not None), stream)
-    L.mtp_block_attn(cache.desc, q, step, B, T, nq, seq_lens, q_lens, block_table, n_table,
-                     cache.desc.hd ** -0.5 if scale is None else scale, out, out_lse, mass, out_mass,
-                     dev_err, ws, ws.nbytes, stream)
+    ws = _with_ws("mtp_block_attn", _block().attn,
+                  _head(cache, q, block_table, seq_lens, q_lens, dev_err, stream),
+                  (scale, out, out_lse, mass, out_mass), ws, cache.device, stream)
     return out, ws
 
 
@@ -403,29 +393,21 @@ def block_select(cache: BlockCache, q, block_table, seq_lens, n_sel, n_first=1, 
                  q_lens=None, out=None, ws=None, dev_err=None, stream=None):
     """The n_sel blocks that each token and kv head attends to, by the 8-bit product of its
     query heads with the blocks' mean keys: (sel [B, T, nkv, n_sel] i32, ws)."""
-    B, T, nq, step, n_table = _queries(cache, q, block_table, seq_lens, q_lens, dev_err)
-    nkv = cache.desc.nkv
-    out = _new((B, T, nkv, n_sel), torch.int32, cache.device, stream) if out is None else out
-    _need(cache.device, torch.int32, B * T * nkv * n_sel, out)
-    ws = _block_ws(cache, ws, L.mtp_block_select_ws_bytes, (B, T, n_table), stream)
-    L.mtp_block_select(cache.desc, q, step, B, T, nq, seq_lens, q_lens, block_table, n_table, n_sel,
-                       n_first, n_last, out, dev_err, ws, ws.nbytes, stream)
+    if out is None:
+        out = _new((*q.shape[:2], cache.desc.nkv, n_sel), torch.int32, cache.device, stream)
+    ws = _with_ws("mtp_block_select", _block().select,
+                  _head(cache, q, block_table, seq_lens, q_lens, dev_err, stream),
+                  (n_sel, n_first, n_last, out), ws, cache.device, stream)
     return out, ws
 
 
 def block_sparse_attn(cache: BlockCache, q, block_table, seq_lens, sel, q_lens=None, scale=None,
                       out=None, out_lse=None, ws=None, dev_err=None, stream=None):
     """block_attn over the blocks that sel [B, T, nkv, n_sel] lists. Returns (out, ws)."""
-    B, T, nq, step, n_table = _queries(cache, q, block_table, seq_lens, q_lens, dev_err)
-    n_sel = sel.shape[3]
-    _need(cache.device, torch.int32, B * T * cache.desc.nkv * n_sel, sel)
     out = _new(q.shape, torch.bfloat16, cache.device, stream) if out is None else out
-    _need(cache.device, torch.bfloat16, q.numel(), out)
-    _need(cache.device, torch.float32, B * T * nq, out_lse)
-    ws = _block_ws(cache, ws, L.mtp_block_sparse_attn_ws_bytes, (B, T, nq, n_sel), stream)
-    L.mtp_block_sparse_attn(cache.desc, q, step, B, T, nq, seq_lens, q_lens, block_table, n_table, sel,
-                            n_sel, cache.desc.hd ** -0.5 if scale is None else scale, out, out_lse,
-                            dev_err, ws, ws.nbytes, stream)
+    ws = _with_ws("mtp_block_sparse_attn", _block().sparse_attn,
+                  _head(cache, q, block_table, seq_lens, q_lens, dev_err, stream),
+                  (sel, scale, out, out_lse), ws, cache.device, stream)
     return out, ws
 
 
@@ -435,18 +417,15 @@ def block_evict(block_table, seq_lens, mass, block_size, keep, n_first=1, n_last
     out_mass, freed, n_freed). Outputs may be the inputs (in place)."""
     B, n_table = block_table.shape
     dev = block_table.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"block_table is on device {dev}, which must be the current one")
     out_table = _new((B, n_table), torch.int32, dev, stream) if out_table is None else out_table
-    freed = _new((B, n_table), torch.int32, dev, stream) if freed is None else freed
     out_lens = _new((B,), torch.int32, dev, stream) if out_lens is None else out_lens
-    n_freed = _new((B,), torch.int32, dev, stream) if n_freed is None else n_freed
     out_mass = _new((B, n_table), torch.float32, dev, stream) if out_mass is None else out_mass
-    _need(dev, torch.int32, B * n_table, block_table, out_table, freed)
-    _need(dev, torch.int32, B, seq_lens, out_lens, n_freed)
-    _need(dev, torch.float32, B * n_table, mass, out_mass)
-    L.mtp_block_evict(B, block_table, n_table, seq_lens, mass, block_size, keep, n_first, n_last,
-                      out_table, out_lens, out_mass, freed, n_freed, stream)
+    freed = _new((B, n_table), torch.int32, dev, stream) if freed is None else freed
+    n_freed = _new((B,), torch.int32, dev, stream) if n_freed is None else n_freed
+    r = _block().evict(block_table, seq_lens, mass, block_size, keep, n_first, n_last, out_table,
+                       out_lens, out_mass, freed, n_freed, L._stream(stream))
+    if r:
+        raise L.MtpError(-r, "mtp_block_evict")
     return out_table, out_lens, out_mass, freed, n_freed
 
 

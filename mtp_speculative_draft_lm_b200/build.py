@@ -1,6 +1,7 @@
 """Builds the CUDA library ``libmtp.so`` in-tree for sm_100a (nvcc cross-compiles
 without a GPU). Each ``csrc/*.cu`` becomes an object, rebuilt only when it or a
-header changed; the objects are linked with the static CUDA runtime."""
+header changed; the objects are linked with the static CUDA runtime. Beside it,
+``_block.so``, the module that makes the block cache's calls from torch tensors."""
 from __future__ import annotations
 
 import glob
@@ -14,6 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmtp.so")
+CALLS_SRC = os.path.join(CSRC, "block_calls.cpp")
+CALLS = os.path.join(PKG, "_block.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -42,14 +45,39 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_calls(force: bool) -> None:
+    newest = max(os.path.getmtime(f) for f in [CALLS_SRC, os.path.join(ROOT, "include", "mtp.h")])
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return
+    import sysconfig
+
+    import torch
+
+    pkg = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(pkg, "include"),
+           os.path.join(pkg, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(a for i in inc for a in ("-isystem", i)), CALLS_SRC, "-o", tmp,
+           "-L" + os.path.join(pkg, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        calls = ex.submit(_build_calls, force)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        calls.result()
     if os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs):
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
