@@ -14,7 +14,10 @@
 // dependent loads (length, block, rows) for single tokens. A warp takes 16 rows of one
 // (sequence, block, head, K or V): its lanes hold 16 bytes of a row each, every row's load is
 // in flight before the first is used, and nothing is read twice. The heads of K and V are the
-// fastest grid dimension, so that a row's bytes are read at about the same time.
+// fastest grid dimension, so that a row's bytes are read at about the same time. A prompt of
+// 32,768 tokens of 8 heads of 128 takes 41 us (4.9 TB/s; 60% of the issue slots: converting and
+// adding up each code), 24 single tokens 3.4 us, 256 of them 7.4 (13.2 with a CTA to a head, three
+// of its four warps idle).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -33,7 +36,8 @@ struct AppendParams {
     const uint16_t* k;
     const uint16_t* v;
     int64_t kv_stride;
-    int touch;  // blocks that T tokens can touch
+    int touch;   // blocks that T tokens can touch
+    int jt_log;  // log2(blocks of one head that a CTA takes at a time)
 };
 
 // Largest magnitude of 2 bf16 each half separately (as integer bits), joined to acc.
@@ -75,10 +79,9 @@ __device__ __forceinline__ void add_codes(float (&sum)[8], const uint2& o) {
         add_halves(sum[2 * u], sum[2 * u + 1], e4m3x2_to_f16x2((uint16_t)(w[u >> 1] >> (16 * (u & 1)))));
 }
 
-// Grid (K or V of each head, groups of touched blocks, sequences). OLD: the earlier rows' codes of
-// a block that already has some are asked for together with the new rows (a step's latency
-// counts: nearly all of its blocks have some), else only once they are needed (a prompt has one
-// such block, and the registers hold more rows in flight instead).
+// Grid (K or V of each head or of several, groups of touched blocks, sequences). OLD: the earlier
+// rows' codes of a block that already has some are asked for together with the new rows, else
+// only once they are needed (and the registers hold more rows in flight instead).
 template <int HD, int BS, bool OLD>
 __global__ void __launch_bounds__(kAppThreads) block_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int WPJ = BS / 16;                // warps per block
@@ -92,7 +95,9 @@ __global__ void __launch_bounds__(kAppThreads) block_append_kernel(const __grid_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wj = warp % WPJ;
     const int sub = lane / LPR, chunk = lane % LPR;
-    const int is_v = blockIdx.x & 1, g = blockIdx.x >> 1, b = blockIdx.z;
+    const int slot = warp / WPJ, jt = 1 << p.jt_log;  // (of JPC) block slots; those of one head
+    const int item = (int)blockIdx.x * (JPC >> p.jt_log) + (slot >> p.jt_log);
+    const int is_v = item & 1, g = item >> 1, b = blockIdx.z;
     pdl_wait();
     pdl_launch_dependents();
     const SeqStep s = seq_step(p.t, b);
@@ -100,11 +105,11 @@ __global__ void __launch_bounds__(kAppThreads) block_append_kernel(const __grid_
     const int first = max(beg, 0) / BS;  // the first touched block
     const uint16_t* x = (is_v ? p.v : p.k) + (int64_t)b * p.t.T * p.kv_stride + (int64_t)g * HD + 8 * chunk;
     const bool mean = !is_v && p.c.k_mean;
-    for (int j0 = (int)blockIdx.y * JPC; j0 < p.touch; j0 += (int)gridDim.y * JPC) {
-        const int j = j0 + warp / WPJ;
+    for (int j0 = (int)blockIdx.y * jt; j0 < p.touch; j0 += (int)gridDim.y * jt) {
+        const int j = j0 + (slot & (jt - 1));
         const int64_t lb = (int64_t)first + j;
         if ((int64_t)(first + j0) * BS >= s.len || s.q == 0) break;  // (the whole CTA's)
-        bool work = j < p.touch && lb * BS < s.len;
+        bool work = g < p.c.nkv && j < p.touch && lb * BS < s.len;
         int phys = -1;
         if (work) {
             phys = table_block(p.t, p.c.num_blocks, b, lb);
@@ -266,25 +271,37 @@ __global__ void __launch_bounds__(kAppThreads) block_append_kernel(const __grid_
     }
 }
 
+template <int HD, int BS>
+cudaError_t launch_bs(const AppendParams& p, dim3 grid, bool old, cudaStream_t s) {
+    return old ? launch_after(block_append_kernel<HD, BS, true>, grid, kAppThreads, 0, s, p)
+               : launch_after(block_append_kernel<HD, BS, false>, grid, kAppThreads, 0, s, p);
+}
+
 template <int HD>
-cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
+cudaError_t launch_append(AppendParams p, cudaStream_t s) {
+    // a CTA's block slots: for one head where a step touches as many blocks or leaves SMs idle all
+    // the same, else for several heads (single tokens of 8 heads: 24 sequences 3.4 us, and 3.5 with
+    // four heads to a CTA; 64 sequences 5.4 and 3.7)
     const int jpc = kAppThreads / 32 / (p.c.bs / 16);
-    const int groups = (p.touch + jpc - 1) / jpc;
-    const dim3 grid((unsigned)(2 * p.c.nkv), (unsigned)(groups < 65535 ? groups : 65535), (unsigned)p.t.B);
-    // (a 16-token step was as fast either way)
-    if (p.t.T <= 16) return p.c.bs == 16 ? launch_after(block_append_kernel<HD, 16, true>, grid, kAppThreads, 0, s, p)
-                          : p.c.bs == 32 ? launch_after(block_append_kernel<HD, 32, true>, grid, kAppThreads, 0, s, p)
-                                         : launch_after(block_append_kernel<HD, 64, true>, grid, kAppThreads, 0, s, p);
-    return p.c.bs == 16 ? launch_after(block_append_kernel<HD, 16, false>, grid, kAppThreads, 0, s, p)
-         : p.c.bs == 32 ? launch_after(block_append_kernel<HD, 32, false>, grid, kAppThreads, 0, s, p)
-                        : launch_after(block_append_kernel<HD, 64, false>, grid, kAppThreads, 0, s, p);
+    const bool few = (int64_t)2 * p.c.nkv * p.t.B <= 4 * 148;
+    while ((1 << p.jt_log) < jpc && (few || (1 << p.jt_log) < p.touch)) ++p.jt_log;
+    const int jt = 1 << p.jt_log, items = jpc >> p.jt_log;
+    const int groups = (p.touch + jt - 1) / jt;
+    const dim3 grid((unsigned)((2 * p.c.nkv + items - 1) / items), (unsigned)(groups < 65535 ? groups : 65535), (unsigned)p.t.B);
+    // OLD while latency counts, which is while the CTAs fit the SMs at once (us with, without:
+    // 24 single tokens of 8 heads 3.4, 4.1; 256 of them 7.4, 7.7, 512 13.3, 11.9; 64 steps of 16
+    // tokens 4.4, 5.1, of 64 10.1, 9.3) and most of a step's blocks have earlier rows (16 steps of
+    // 64 tokens 4.5, 5.0, of 128 6.1, 5.5; a prompt of 32,768 45.8, 41.4)
+    const bool old = p.t.T <= 64 && (int64_t)grid.x * grid.y * grid.z <= 1024;
+    return p.c.bs == 16 ? launch_bs<HD, 16>(p, grid, old, s) : p.c.bs == 32 ? launch_bs<HD, 32>(p, grid, old, s)
+                                                                            : launch_bs<HD, 64>(p, grid, old, s);
 }
 
 }  // namespace
 
 cudaError_t block_append_launch(const BlockCache& c, const BlockBatch& t, const uint16_t* k,
                                 const uint16_t* v, int64_t kv_stride, cudaStream_t s) {
-    AppendParams p{c, t, k, v, kv_stride, 0};
+    AppendParams p{c, t, k, v, kv_stride, 0, 0};
     p.touch = (int)((t.T + c.bs - 2) / c.bs + 1);
     if (p.touch > t.n_table) p.touch = (int)t.n_table + 1;  // one more, whose tokens are flagged
     return c.hd == 64 ? launch_append<64>(p, s) : c.hd == 128 ? launch_append<128>(p, s) : launch_append<256>(p, s);
