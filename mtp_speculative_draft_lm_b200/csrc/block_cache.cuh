@@ -49,14 +49,14 @@ constexpr float kInv127 = 1.f / 127.f;
 // The `want` smallest of a list of keys in (key, index) order, by one CTA of THREADS threads that
 // hold KEYS keys each, key u of thread t being entry u THREADS + t (whole rows of loads and
 // stores). Digits are counted from the top among the keys that share the digits found so far
-// until a count ends exactly at `want`: of 8 bits for 256 threads, of 11 for 1,024 (2.7 and 3.4
+// until a count ends exactly at `want`: of 8 bits for 256 threads, of 11 for more (2.7 and 3.4
 // thousand cycles for 512 and 2,048 spread floats, 6.3 for 8,192; most of it barriers). Integer
 // counts: the choice is exact.
 template <int THREADS>
 struct PickSmem {
     static constexpr int kBits = THREADS <= 256 ? 8 : 11, kBins = 1 << kBits, kWarps = THREADS / 32;
     uint32_t hist[kBins];
-    uint32_t tot[kWarps * 8];  // taken in each warp's row of 32 entries, then before it
+    uint32_t tot[256];  // taken in each warp's row of 32 entries, then before it
     uint32_t warp_sum[32];
     uint32_t digit, before, in_digit;
 };
@@ -137,8 +137,8 @@ __device__ __forceinline__ void pick_threshold(const Each& each, uint32_t want, 
 template <int THREADS, int KEYS>
 __device__ __forceinline__ void pick_places(const uint32_t (&k)[KEYS], int n, uint32_t thr, uint32_t need, PickSmem<THREADS>& sm,
                                             uint32_t* taken, uint32_t (&before)[KEYS]) {
-    static_assert(KEYS <= 8, "sm.tot");
-    constexpr int W = THREADS / 32, N = KEYS * W;  // rows of 32 entries, in index order
+        constexpr int W = THREADS / 32, N = KEYS * W;  // rows of 32 entries, in index order
+    static_assert(N <= 256, "sm.tot");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t below = (1u << lane) - 1u;
 #pragma unroll

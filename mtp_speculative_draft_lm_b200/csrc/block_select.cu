@@ -13,7 +13,7 @@
 // lanes issue theirs one after the other), a ring of 16-byte copies 48.
 // The choice is one CTA for each token and head, its keys in registers: a search for the last
 // chosen key, then one prefix sum that gives every chosen block its place in the ascending list;
-// 256 lists of 256 from up to 8,192 blocks take 11 us, most of it the search's barriers.
+// 256 lists of 256 from up to 8,192 blocks take 10 us, most of it the search's barriers.
 //
 // Eviction: the same choice of the smallest accumulated weights by one CTA per sequence, whose
 // prefix sum moves the table and the weights up, in place where asked (256 sequences of up to
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_co
 // One CTA per (sequence, token, kv head). ALL: the CTA holds every key (n_table <= THREADS KEYS);
 // else they are read again (from L2) for each digit and then in order, THREADS KEYS at a time.
 template <int THREADS, int KEYS, bool ALL>
-__global__ void __launch_bounds__(THREADS, 2048 / THREADS) block_choose_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(THREADS, KEYS == 16 ? 2 : 2048 / THREADS) block_choose_kernel(const __grid_constant__ SelectParams p) {
     __shared__ PickSmem<THREADS> sm;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
@@ -397,10 +397,14 @@ cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const 
                                 : launch_after(block_score_kernel<256>, grid, kScThreads, 0, s, p);
     if (e != cudaSuccess) return e;
     const dim3 g2((unsigned)rows);
-    // the fewest threads and keys that hold the table
+    // The fewest threads and keys that hold the table. A barrier of 512 threads costs less than one
+    // of 1,024 where several CTAs share an SM (us for scores and choice: 256 rows of up to 8,192
+    // blocks 36.6, and 38.1 with 1,024 threads; 512 rows of 2,048 27.1 and 29.5), and a CTA alone
+    // on its SM is faster with more threads (128 rows of 2,048 16.2 and 15.5).
     if (t.n_table <= 512) return launch_after(block_choose_kernel<256, 2, true>, g2, 256, 0, s, p);
-    if (t.n_table <= 2048) return launch_after(block_choose_kernel<1024, 2, true>, g2, 1024, 0, s, p);
-    if (t.n_table <= 8192) return launch_after(block_choose_kernel<1024, 8, true>, g2, 1024, 0, s, p);
+    if (t.n_table <= 2048 && rows <= 2 * 148) return launch_after(block_choose_kernel<1024, 2, true>, g2, 1024, 0, s, p);
+    if (t.n_table <= 2048) return launch_after(block_choose_kernel<512, 4, true>, g2, 512, 0, s, p);
+    if (t.n_table <= 8192) return launch_after(block_choose_kernel<512, 16, true>, g2, 512, 0, s, p);
     return launch_after(block_choose_kernel<1024, 8, false>, g2, 1024, 0, s, p);
 }
 
