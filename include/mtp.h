@@ -443,9 +443,10 @@ mtp_status mtp_paged_decode_attn(const uint16_t* q, int32_t nq, int32_t nkv, int
  *   block >= n_table, physical one outside [0, num_blocks)) is skipped and sets
  *   MTP_DEVFLAG_BAD_SLOT in dev_err (device i32 [1] or NULL).
  * Requires hd in {64, 128, 256}, block_size in {16, 32, 64}, 1 <= B <= 65535, nkv <= 4096,
- * num_blocks < 2^31, n_table * block_size <= 2^30 (MTP_ERR_UNSUPPORTED otherwise); codes, means and bf16 tensors 16-byte
- * aligned, cache strides positive multiples of 16 bytes with row_stride >= hd, bf16 token
+ * num_blocks < 2^31, n_table * block_size <= 2^30 (MTP_ERR_UNSUPPORTED otherwise); codes, means
+ * and bf16 tensors 16-byte aligned, cache strides positive multiples of 16 bytes with row_stride >= hd, bf16 token
  * strides multiples of 8 elements. Rows of different sequences may share blocks that are only read.
+ * The *_ws_bytes functions give 0 for sizes that their call refuses.
  * ------------------------------------------------------------------------------ */
 typedef struct {
     int32_t nkv;
@@ -493,8 +494,9 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
  *   logical block j of w_p, for every j < n_table
  * fp32 sums and softmax statistics; the tensor cores take q as f16 scaled per head by a power
  * of two (exact for elements above 2^-31 of the head's largest) and the weights
- * exp(s_p - reference) rounded to f16 (denominator, lse and mass sum them unrounded). A token that sees no readable position gets zeros, lse -inf and no
- * mass. What lies in masked rows (NaN included) changes nothing.
+ * exp(s_p - reference) rounded to f16 (denominator, lse and mass sum them unrounded). A token
+ * that sees no readable position gets zeros, lse -inf and no mass. What lies in masked rows (NaN
+ * included) changes nothing.
  *   q        (device) bf16 [B, T, nq, hd], consecutive tokens q_stride elements apart
  *            (>= nq * hd), sequences T * q_stride apart
  *   out      (device) bf16 [B, T, nq, hd] contiguous; out_lse f32 [B, T, nq] or NULL
@@ -502,9 +504,9 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
  *            buffer; mass without out_mass is MTP_ERR_INVALID_ARG)
  *   ws       (device) >= mtp_block_attn_ws_bytes(cache, B, T, nq, n_table, with_mass) bytes,
  *            16-byte aligned, no initial contents; with_mass = out_mass != NULL
- * Requires nq % nkv == 0, nq / nkv <= 16, 1 <= T <= 64, scale >= 0, and fewer than 2^31 tiles of 16
- * positions over all sequences at n_table blocks each, kv heads and groups of at least 8 of a
- * head's T nq / nkv query rows (MTP_ERR_UNSUPPORTED otherwise). Results do not depend on
+ * Requires nq % nkv == 0, nq / nkv <= 16, 1 <= T <= 64, scale >= 0, and fewer than 2^31 tiles of
+ * 16 positions (and 12 more per unit) over all units: sequences at n_table blocks each, kv heads
+ * and groups of at least 8 of a head's T nq / nkv query rows (MTP_ERR_UNSUPPORTED otherwise). Results do not depend on
  * the order in which blocks of the grid run: the same call gives the same bits. */
 size_t mtp_block_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T, int32_t nq,
                                int64_t n_table, int32_t with_mass);
@@ -539,7 +541,8 @@ mtp_status mtp_block_select(const mtp_block_cache* cache, const uint16_t* q, int
  * the positions p < lim(b, t) of the logical blocks sel[b, t, g, :] (i32 [B, T, nkv, n_sel], as
  * mtp_block_select writes it; negative entries are skipped, order does not matter, a block
  * listed twice counts twice). No mass. ws >= mtp_block_sparse_attn_ws_bytes(...) bytes;
- * n_sel * block_size <= 2^30, fewer than 2^31 listed 16-position tiles; every other argument and rule is mtp_block_attn's. */
+ * n_sel * block_size <= 2^30, fewer than 2^31 listed 16-position tiles (and 12 more for each token
+ * and kv head); every other argument and rule is mtp_block_attn's. */
 size_t mtp_block_sparse_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
                                       int32_t nq, int32_t n_sel);
 mtp_status mtp_block_sparse_attn(const mtp_block_cache* cache, const uint16_t* q,

@@ -423,6 +423,15 @@ mtp_status check_block_query(const mtp_block_cache* c, const uint16_t* q, int64_
     return MTP_OK;
 }
 
+// Whether a workspace size has a meaning: what the calls themselves allow.
+bool sized(const mtp_block_cache* c, int32_t B, int32_t T, int64_t n_table) {
+    return check_block_cache(c, false, false) == MTP_OK && B >= 1 && B <= 65535 && T >= 1 &&
+           T <= mtp::block_attn_max_t() && n_table >= 1 && n_table <= ((int64_t)1 << 30) / c->block_size;
+}
+bool grouped(const mtp_block_cache* c, int32_t nq) {
+    return nq >= 1 && nq % c->nkv == 0 && nq / c->nkv <= mtp::block_attn_max_group();
+}
+
 mtp::BlockCache to_cache(const mtp_block_cache* c) {
     return {c->nkv, c->hd, c->block_size, c->num_blocks, c->block_stride, c->head_stride, c->row_stride,
             c->k, c->v, c->k_scale, c->v_scale, c->k_mean, c->k_mean_scale};
@@ -474,7 +483,7 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
 
 size_t mtp_block_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T, int32_t nq,
                                int64_t n_table, int32_t with_mass) {
-    if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || nq < 1 || n_table < 1) return 0;
+    if (!sized(cache, B, T, n_table) || !grouped(cache, nq)) return 0;
     return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, n_table, false, with_mass != 0);
 }
 
@@ -490,7 +499,7 @@ mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64
 
 size_t mtp_block_sparse_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
                                       int32_t nq, int32_t n_sel) {
-    if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || nq < 1 || n_sel < 1) return 0;
+    if (!sized(cache, B, T, n_sel) || !grouped(cache, nq)) return 0;
     return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, 1, true, false);
 }
 
@@ -507,7 +516,7 @@ mtp_status mtp_block_sparse_attn(const mtp_block_cache* cache, const uint16_t* q
 
 size_t mtp_block_select_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
                                  int64_t n_table) {
-    if (check_block_cache(cache, false, false) != MTP_OK || B < 1 || T < 1 || n_table < 1) return 0;
+    if (!sized(cache, B, T, n_table)) return 0;
     return mtp::block_select_ws_bytes(to_cache(cache), B, T, n_table);
 }
 

@@ -140,3 +140,14 @@ def test_python_layouts():
     for bad in (t.float(), t.transpose(1, 2), fused[:, :2, :256].unflatten(-1, (4, 64)), t[..., ::2]):
         with pytest.raises(ValueError):
             api._token_stride(bad)
+
+
+def test_workspace_sizes_of_refused_calls():
+    """Sizes that a call refuses (fewer query heads than kv heads among them) need no workspace."""
+    lib, c = L.load(), C.byref(cache())
+    assert lib.mtp_block_attn_ws_bytes(c, 2, 3, 64, 10, 0) > 0 and lib.mtp_block_sparse_attn_ws_bytes(c, 2, 3, 64, 4) > 0
+    for nq in (-8, 0, 1, 4, 7, 60, 136):
+        assert lib.mtp_block_attn_ws_bytes(c, 2, 3, nq, 10, 1) == lib.mtp_block_sparse_attn_ws_bytes(c, 2, 3, nq, 4) == 0
+    for B, T, n in ((0, 3, 10), (65536, 3, 10), (2, 0, 10), (2, 65, 10), (2, 3, 0), (2, 3, (1 << 26) + 1), (-1, 3, 10)):
+        assert lib.mtp_block_attn_ws_bytes(c, B, T, 64, n, 0) == lib.mtp_block_select_ws_bytes(c, B, T, n) == 0
+        assert lib.mtp_block_sparse_attn_ws_bytes(c, B, T, 64, n) == 0

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import block_ref as R
+from mtp_speculative_draft_lm_b200 import _lib as L
 from mtp_speculative_draft_lm_b200 import api
 from test_gpu_block_cache import batch, bf16, err_word, i32, make_cache, same_cache, to_gpu
 from test_gpu_block_cache_use import outputs, step_state
@@ -66,6 +67,22 @@ def test_native_calls_refuse_what_is_no_tensor():
     for f in (lambda: api.block_attn(ca, q, tab, lens, out=q, scale="1"), lambda: api.block_select(ca, q, tab, lens, 4.5, out=st["o"]["sel"])):
         with pytest.raises(TypeError):
             f()
+
+
+def test_refused_sizes_raise():
+    """Fewer query heads than kv heads, too many tokens: an error from the call, with a workspace or
+    without one."""
+    st = outputs(step_state(np.random.default_rng(6)))
+    ca, q, tab, lens = st["cache"], st["q"], st["table"], st["lens"]
+    wide = torch.zeros((3, 65, 8, 128), dtype=torch.bfloat16, device="cuda")
+    for x, status in ((q[:, :, :1].contiguous(), L.MTP_ERR_INVALID_ARG), (wide, L.MTP_ERR_UNSUPPORTED)):
+        sel = torch.zeros((3, x.shape[1], 2, 4), dtype=torch.int32, device="cuda")
+        for ws in (None, torch.empty(1 << 20, dtype=torch.uint8, device="cuda")):
+            for f in (lambda: api.block_attn(ca, x, tab, lens, ws=ws), lambda: api.block_select(ca, x, tab, lens, 4, ws=ws),
+                      lambda: api.block_sparse_attn(ca, x, tab, lens, sel, ws=ws)):
+                with pytest.raises(L.MtpError) as e:
+                    f()
+                assert e.value.status == status
 
 
 def test_threads_call_at_once():
