@@ -64,6 +64,12 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Bytes between the 8-bit query rows in shared memory: two rows' 64-byte pieces in other banks.
 template <int HD>
 __host__ __device__ constexpr int q8_pitch() { return HD == 64 ? 64 : HD + 64; }
@@ -124,19 +130,27 @@ __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_co
             for (int o = LPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             const bool odd = !has || top >= 0x7f80u;  // no head, or one with an infinity or NaN
             const float sc = odd ? 0.f : __fmul_rn(bf16_to_f32((uint16_t)top), kInv127);
-            // rint(v / sc): by the reciprocal, and by the division itself where that is within
-            // 10^-4 of a half (its error is below 3 10^-5) or the scale is tiny
+            // rint(v / sc), as the units of a float 1.5 2^23 above: by the reciprocal, and by the
+            // division itself where one of the values is within 10^-4 of a half (the product's
+            // error is below 5 10^-5) or the scale is tiny
             const bool tiny = sc < 1e-30f;
-            const float inv = tiny ? 0.f : __fdiv_rn(1.f, sc);
-            uint32_t w[2] = {0, 0};
+            const float inv = tiny ? 0.f : reciprocal(sc);
+            float d[8], far = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float v = k & 1 ? bf16_hi(xw[k >> 1]) : bf16_lo(xw[k >> 1]);
-                float n = rintf(v * inv);
-                if (sc > 0.f && (tiny || fabsf(fabsf(v * inv - n) - 0.5f) < 1e-4f)) n = rintf(__fdiv_rn(v, sc));
-                w[k >> 2] |= ((uint32_t)(int)n & 255u) << (8 * (k & 3));
+                d[k] = odd ? 12582912.f : fmaf(v, inv, 12582912.f);
+                far = fmaxf(far, fabsf(fmaf(v, inv, 12582912.f - d[k])));
             }
-            if (!(sc > 0.f)) w[0] = w[1] = 0;
+            if (sc > 0.f && (tiny || far > 0.4999f))
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    d[k] = rintf(__fdiv_rn(k & 1 ? bf16_hi(xw[k >> 1]) : bf16_lo(xw[k >> 1]), sc)) + 12582912.f;
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                w[k] = __byte_perm(__byte_perm(__float_as_uint(d[4 * k]), __float_as_uint(d[4 * k + 1]), 0x0040),
+                                   __byte_perm(__float_as_uint(d[4 * k + 2]), __float_as_uint(d[4 * k + 3]), 0x0040), 0x5410);
             *reinterpret_cast<uint2*>(q8 + r * q8_pitch<HD>() + 8 * l) = make_uint2(w[0], w[1]);
             if (l == 0) sq[r] = odd ? make_float2(0.f, -INFINITY) : make_float2(sc, 0.f);
         }
