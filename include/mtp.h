@@ -445,7 +445,9 @@ mtp_status mtp_paged_decode_attn(const uint16_t* q, int32_t nq, int32_t nkv, int
  * Requires hd in {64, 128, 256}, block_size in {16, 32, 64}, 1 <= B <= 65535, nkv <= 4096,
  * num_blocks < 2^31, n_table * block_size <= 2^30 (MTP_ERR_UNSUPPORTED otherwise); codes, means
  * and bf16 tensors 16-byte aligned, cache strides positive multiples of 16 bytes with row_stride >= hd, bf16 token
- * strides multiples of 8 elements. Rows of different sequences may share blocks that are only read.
+ * strides multiples of 8 elements. Sequences may share blocks that are only read; a block that an
+ * append writes to belongs to one logical block of one sequence (with more, which of the rows
+ * remain is undefined; nothing else is touched). Outputs overlap inputs only where a call says so.
  * The *_ws_bytes functions give 0 for sizes that their call refuses.
  * ------------------------------------------------------------------------------ */
 typedef struct {

@@ -113,6 +113,28 @@ __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_co
         const int t1 = min(s.q, t0 + chunk), rows = (t1 - t0) * gr;
         int next[4];
         look_up(j_first, next);
+        // two tiles of 16 blocks; rows gid and gid + 8 of tile u: blocks j0 + gid + 8 (2 u + {0, 1})
+        uint4 m[4][C];
+        float sk[4];
+        uint32_t has = 0;
+        auto fetch = [&](int j0) {  // the blocks looked up last; those after them are looked up
+            has = 0;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                sk[h] = 0.f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) m[h][c] = make_uint4(0, 0, 0, 0);
+                if (next[h] >= 0) {
+                    has |= 1u << h;
+                    const int64_t at = (int64_t)next[h] * p.c.nkv;
+                    sk[h] = scales[at];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) m[h][c] = ldg_stream(means + at * HD + 64 * c);
+                }
+            }
+            if (j0 + kPartBlocks < j_end) look_up(j0 + kPartBlocks, next);
+        };
+        fetch(j_first);  // (they arrive while the query rows are quantized)
         if (t0) __syncthreads();  // the earlier rows have been used
         // HD / 8 lanes per row, 8 values each: one load and one pass for 16 rows of 128
         constexpr int LPR = HD / 8, RPW = 32 / LPR;
@@ -156,24 +178,7 @@ __global__ void __launch_bounds__(kScThreads) block_score_kernel(const __grid_co
         }
         __syncthreads();
         for (int j0 = j_first; j0 < j_end; j0 += kPartBlocks) {
-            // two tiles of 16 blocks; rows gid and gid + 8 of tile u: blocks j0 + gid + 8 (2 u + {0, 1})
-            uint4 m[4][C];
-            float sk[4];
-            uint32_t has = 0;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                sk[h] = 0.f;
-#pragma unroll
-                for (int c = 0; c < C; ++c) m[h][c] = make_uint4(0, 0, 0, 0);
-                if (next[h] >= 0) {
-                    has |= 1u << h;
-                    const int64_t at = (int64_t)next[h] * p.c.nkv;
-                    sk[h] = scales[at];
-#pragma unroll
-                    for (int c = 0; c < C; ++c) m[h][c] = ldg_stream(means + at * HD + 64 * c);
-                }
-            }
-            if (j0 + kPartBlocks < j_end) look_up(j0 + kPartBlocks, next);
+            if (j0 > j_first) fetch(j0);
             // lane tig of a row's four writes block j0 + gid + 8 tig
             const int j = j0 + gid + 8 * tig;
             uint32_t* out = keys + t0 * key_step + j;
