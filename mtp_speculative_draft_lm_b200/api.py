@@ -342,12 +342,17 @@ def _token_stride(x: torch.Tensor) -> int:
 
 
 def _new(shape, dtype, device: int, stream):
-    """A tensor for a call on `stream` (None: the current one)."""
+    """A tensor that a call on `stream` writes (None: the current one): that stream's memory, whose
+    earlier use its work comes after, and not given back before the current stream's use ends."""
     if device < 0:
         raise ValueError("the tensors must be on a GPU")
-    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
-    if isinstance(stream, torch.cuda.Stream):
-        t.record_stream(stream)
+    dev = torch.device("cuda", device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 

@@ -111,3 +111,23 @@ def test_threads_call_at_once():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "address"])
+def test_new_outputs_are_the_streams_own(raw):
+    """A call on another stream does not write into memory that the current stream's work, still
+    to run, has yet to write."""
+    st = step_state(np.random.default_rng(8))
+    ca, q, tab, lens = st["cache"], st["q"], st["table"], st["lens"]
+    want, ws = api.block_attn(ca, q, tab, lens)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        late = [torch.empty_like(want) for _ in range(4)]
+        torch.cuda._sleep(20_000_000)  # (10 ms)
+        for t in late:
+            t.fill_(7)
+        del late, t
+        out, _ = api.block_attn(ca, q, tab, lens, ws=ws, stream=s.cuda_stream if raw else s)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
