@@ -312,12 +312,24 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) block_evict_kernel(co
     const int n = (int)p.n_table;
     pdl_wait();
     pdl_launch_dependents();
-    const int len = max(p.lens[b], 0);
-    const int nb = blocks_of(len, p.bs, n);
-    const int go = max(nb - p.keep, 0);
     const int64_t base_at = (int64_t)b * p.n_table;
     const int32_t* table = p.table + base_at;
     const float* mass = p.mass + base_at;
+    // A short table is read whole while the length is on its way and stays in registers (8
+    // sequences of 500 blocks: 3.6 us, 3.9 with reads after the length and after the choice)
+    constexpr bool EARLY = ALL && KEYS <= 2;
+    int32_t blk0[EARLY ? KEYS : 1];
+    float m0[EARLY ? KEYS : 1];
+    if (EARLY)
+#pragma unroll
+        for (int u = 0; u < KEYS; ++u) {
+            const int i = u * THREADS + tid;
+            blk0[EARLY ? u : 0] = i < n ? table[i] : 0;
+            m0[EARLY ? u : 0] = i < n ? mass[i] : 0.f;
+        }
+    const int len = max(p.lens[b], 0);
+    const int nb = blocks_of(len, p.bs, n);
+    const int go = max(nb - p.keep, 0);
     int32_t* out_table = p.out_table + base_at;
     float* out_mass = p.out_mass + base_at;
     int32_t* freed = p.freed + base_at;
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) block_evict_kernel(co
 #pragma unroll
         for (int u = 0; u < KEYS; ++u) {
             const int i = base + u * THREADS + tid;
-            k[u] = i < p.n_first || i >= nb - p.n_last ? 0xffffffffu : order_key(mass[i]);
+            k[u] = i < p.n_first || i >= nb - p.n_last ? 0xffffffffu : order_key(EARLY ? m0[EARLY ? u : 0] : mass[i]);
         }
     };
     uint32_t k[KEYS], thr = 0, need = 0, before[KEYS] = {}, taken = 0;
@@ -355,10 +367,10 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) block_evict_kernel(co
 #pragma unroll
             for (int u = 0; u < G; ++u) {
                 const int i = base + (u0 + u) * THREADS + tid;
-                blk[u] = i < nb ? table[i] : 0;
-                m[u] = i < nb ? mass[i] : 0.f;
+                blk[u] = EARLY ? blk0[EARLY ? u0 + u : 0] : i < nb ? table[i] : 0;
+                m[u] = EARLY ? m0[EARLY ? u0 + u : 0] : i < nb ? mass[i] : 0.f;
             }
-            __syncthreads();
+            if (!EARLY) __syncthreads();
 #pragma unroll
             for (int u = 0; u < G; ++u) {
                 const int i = base + (u0 + u) * THREADS + tid, gone = done + (int)before[u0 + u];
