@@ -370,14 +370,20 @@ def _with_ws(where: str, call, head: tuple, tail: tuple, ws, device: int, stream
 
 def _head(cache: BlockCache, x, block_table, seq_lens, q_lens, dev_err, stream) -> tuple:
     return (C.addressof(cache.desc), cache.device, x, block_table, seq_lens, q_lens, dev_err,
-            L._stream(stream))
+            _address(stream))
+
+
+def _address(stream):
+    """The stream as _block takes it (None: the current one, which it looks up itself)."""
+    return None if stream is None else L._stream(stream)
 
 
 def block_append(cache: BlockCache, k, v, block_table, seq_lens, q_lens=None, dev_err=None,
                  stream=None):
     """Writes the new rows k, v [B, T, nkv, hd] (bf16, slices of a projection allowed) at the end
     of each sequence (seq_lens counts them already) and updates scales and means."""
-    r = _block().append(*_head(cache, k, block_table, seq_lens, q_lens, dev_err, stream), v)
+    r = _block().append(C.addressof(cache.desc), cache.device, k, block_table, seq_lens, q_lens,
+                        dev_err, _address(stream), v)
     if r:
         raise L.MtpError(-r, "mtp_block_append")
 
@@ -428,7 +434,7 @@ def block_evict(block_table, seq_lens, mass, block_size, keep, n_first=1, n_last
     freed = _new((B, n_table), torch.int32, dev, stream) if freed is None else freed
     n_freed = _new((B,), torch.int32, dev, stream) if n_freed is None else n_freed
     r = _block().evict(block_table, seq_lens, mass, block_size, keep, n_first, n_last, out_table,
-                       out_lens, out_mass, freed, n_freed, L._stream(stream))
+                       out_lens, out_mass, freed, n_freed, _address(stream))
     if r:
         raise L.MtpError(-r, "mtp_block_evict")
     return out_table, out_lens, out_mass, freed, n_freed

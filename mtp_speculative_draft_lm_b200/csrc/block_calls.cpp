@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -66,6 +67,11 @@ struct Args {
         if (v == -1.0 && PyErr_Occurred()) throw Raised();
         return v;
     }
+    void* stream(int64_t device) {  // None: the current one of the device
+        if (*at != Py_None) return address();
+        ++at;
+        return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
+    }
     void* address() {  // None: null
         PyObject* o = next();
         if (o == Py_None) return nullptr;
@@ -113,11 +119,11 @@ struct Call {
         device = a.integer();
         x = a.tensor();
         const at::Tensor *t = a.tensor(), *l = a.tensor(), *q = a.tensor(), *e = a.tensor();
-        stream = a.address();
         if (!cache || !x || !t || !l) throw Refused("tokens, block_table and seq_lens are needed");
         if (x->get_device() != device || device < 0 || device != c10::cuda::current_device())
             throw Refused("the cache is on device " + std::to_string(device) + ", the tokens on " + std::to_string(x->get_device()) +
                           "; both must be the current one");
+        stream = a.stream(device);
         step = token_stride(*x);
         B = x->size(0), T = x->size(1), heads = x->size(2);
         if (x->size(3) != cache->hd)
@@ -263,7 +269,7 @@ PyObject* py_evict(PyObject*, PyObject* const* args, Py_ssize_t n) {
         float* out_mass = floats(a.tensor());
         int32_t* freed = ints(a.tensor(), B * n_table);
         int32_t* n_freed = ints(a.tensor(), B);
-        void* stream = a.address();
+        void* stream = a.stream(device);
         const Unlocked u;
         return -(int64_t)abi.evict((int32_t)B, table_at, n_table, lens_at, mass_at, bs, keep, n_first, n_last, out_table, out_lens,
                                    out_mass, freed, n_freed, stream);
