@@ -496,7 +496,9 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
  *   logical block j of w_p, for every j < n_table
  * fp32 sums and softmax statistics; the tensor cores take q as f16 scaled per head by a power
  * of two (exact for elements above 2^-31 of the head's largest) and the weights
- * exp(s_p - reference) rounded to f16 (denominator, lse and mass sum them unrounded). A token
+ * exp(s_p - reference) rounded to f16, each to within 2^-11 of itself or 2^-27 of the row's largest
+ * weight, whichever is more (for v_scales within 2^90 of the sequence's largest; denominator, lse
+ * and mass sum them unrounded). A token
  * that sees no readable position gets zeros, lse -inf and no mass. What lies in masked rows (NaN
  * included) changes nothing.
  *   q        (device) bf16 [B, T, nq, hd], consecutive tokens q_stride elements apart

@@ -6,10 +6,15 @@
 // with any reference m: a running one, raised only when a score exceeds it by more than 8
 // binades (weights stay below 2^8, inside f16), so that most tiles need no maximum, no shuffle
 // and no rescaling, just one vote. A block's v_scale is not folded into the weights (they would
-// lose f16 bits where scales lie far apart): the accumulators are held in units of an earlier
-// block's v_scale, weights are multiplied by v_scale / unit before they are rounded, and the
-// unit moves when that leaves [2^-10, 2^6] (weights below 2^14 fit f16, and what a rounding to
-// its smallest steps takes, 2^-25, is 2^-15 of the block's largest weight at most).
+// lose f16 bits where scales lie far apart): the accumulators are held in a unit near the v_scales,
+// weights are multiplied by v_scale / unit before they are rounded to f16, and the unit moves when
+// that leaves [2^2, 2^7]: weights of at most 2^15 fit f16, and a rounding to f16's smallest steps
+// takes 2^-27 of the row's largest weight at most (a row's largest is 1 or more before it is
+// multiplied), counted in the block's own v_scale. The unit follows the smaller scales, so that
+// a block of small values behind one of large values keeps its part: with v_scale / unit down
+// to 2^-10 the tail behind a position that has most of the weight was rounded away (67 times the
+// error that the test allows). Scales within a factor of 32 of each other move the unit a few
+// times at most.
 //
 // Work: the cache is read in tiles of 16 positions, each inside one block. A unit is a kv head
 // of a sequence with up to 8 NT of its T (nq / nkv) query rows (for listed blocks: of a
@@ -56,6 +61,7 @@ constexpr int kMaxGrid = 640;                  // CTAs (workspace slots are size
 // had the short ones were the last by a third of that (44 us with 12 or 16, 45 with 8, 48 with 32).
 constexpr int kUnitCost = 12;
 constexpr float kRaise = 8.f;                  // binades a score may exceed the reference by
+constexpr float kLeastLift = 4.f, kMostLift = 128.f;  // v_scale over the accumulators' unit (kRaise and 7 binades: f16)
 
 struct AttnParams {
     BlockCache c;
@@ -648,14 +654,16 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, NT>::kPerSm)
                 for (int z = 0; z < HJ; ++z) {
                     // the block's v_scale over the accumulators' unit
                     float wmul = vs[z] * vinv;
-                    if (!(wmul >= 9.765625e-4f && wmul <= 64.f) && pos0[z] != kNowhere) {
-                        // a new unit: the block's v_scale, but never more than 2^90 below the
-                        // largest so far (the sums would overflow); a zero scale weighs nothing
+                    if (!(wmul >= kLeastLift && wmul <= kMostLift) && pos0[z] != kNowhere) {
+                        // a new unit: as far below the block's v_scale as the side it left by asks for, but
+                        // a normal number, and never more than 2^92 below the largest v_scale so far (the
+                        // sums would overflow); a zero scale weighs nothing
                         if (vs[z] == 0.f) {
                             wmul = 0.f;
                         } else {
                             vmax = fmaxf(vmax, vs[z]);
-                            const float unit = fmaxf(vs[z], vmax * 8.077935669463161e-28f);
+                            const float unit = fmaxf(fmaxf(vs[z] * (wmul > kMostLift ? 1.f / kMostLift : 1.f / kLeastLift), vmax * 2.0194839173657902e-28f),
+                                                     1.17549435e-38f);
                             wmul = vs[z] / unit;
                             const float ratio = vcur / unit;
                             vcur = unit;
