@@ -341,6 +341,15 @@ def _token_stride(x: torch.Tensor) -> int:
     return _block().token_stride(x)
 
 
+def _torch_stream(stream, device: torch.device):
+    """A stream argument (a torch stream or an address; 0 is the default stream) as torch's object."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    address = L._stream(stream)
+    # (torch takes an external address of 0 for none at all, and gives a stream of its pool)
+    return torch.cuda.ExternalStream(address, device=device) if address else torch.cuda.default_stream(device)
+
+
 def _new(shape, dtype, device: int, stream):
     """A tensor that a call on `stream` writes (None: the current one): that stream's memory, whose
     earlier use its work comes after, and not given back before the current stream's use ends."""
@@ -349,8 +358,7 @@ def _new(shape, dtype, device: int, stream):
     dev = torch.device("cuda", device)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, device=dev)
-    with torch.cuda.stream(s):
+    with torch.cuda.stream(_torch_stream(stream, dev)):
         t = torch.empty(shape, dtype=dtype, device=dev)
     t.record_stream(torch.cuda.current_stream(dev))
     return t
