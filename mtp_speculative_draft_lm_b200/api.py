@@ -268,7 +268,11 @@ def _need(device: int, dtype, numel: int, *tensors):
 class BlockCache:
     """A block-scaled paged cache: E4M3 codes k, v with logical shape [num_blocks, nkv,
     block_size, hd] (uint8, any strides with hd contiguous), fp32 scales [num_blocks, nkv] and,
-    for block selection, 8-bit mean keys [num_blocks, nkv, hd] with their scales."""
+    for block selection, 8-bit mean keys [num_blocks, nkv, hd] with their scales.
+
+    The block_* calls run on the current stream, or on their argument `stream` (a torch stream or
+    its address): the caller orders that one behind what writes their inputs and before what
+    reads their outputs; any tensor of the call may be let go as soon as it returns."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
@@ -288,9 +292,10 @@ class BlockCache:
         _need(self.device, torch.float32, nb * nkv, self.k_scale, self.v_scale, self.k_mean_scale)
         _need(self.device, torch.int8, nb * nkv * hd, self.k_mean)
         self.desc = L.mtp_block_cache(nkv, hd, bs, 0, nb, self.k.stride(0), self.k.stride(1),
-                                      self.k.stride(2), *(L._ptr(t) for t in (
-                                          self.k, self.v, self.k_scale, self.v_scale, self.k_mean,
-                                          self.k_mean_scale)))
+                                      self.k.stride(2), *(L._ptr(t) for t in self.tensors()))
+
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale, self.k_mean, self.k_mean_scale
 
     @classmethod
     def empty(cls, num_blocks: int, nkv: int, hd: int, block_size: int = 16, device="cuda"):
@@ -364,19 +369,33 @@ def _new(shape, dtype, device: int, stream):
     return t
 
 
-def _with_ws(where: str, call, head: tuple, tail: tuple, ws, device: int, stream):
+def _used_on(stream, device: int, *tensors):
+    """Tells the allocator that a call on `stream` (None: the current one, as any torch call) uses these
+    tensors: one that the caller lets go while the call runs is not handed out before it has ended."""
+    if stream is not None:
+        s = _torch_stream(stream, torch.device("cuda", device))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def _with_ws(where: str, call, cache: BlockCache, head: tuple, tail: tuple, ws, stream):
     """Makes a call whose last argument is its workspace, with a new one if ws is None or too
     small (the call then says how large, and launches nothing); returns the workspace."""
-    r = call(*head, *tail, ws)
+    args = _call(cache, *head, stream) + tail
+    r = call(*args, ws)
     if r > 0:
-        ws = _new((r,), torch.uint8, device, stream)
-        r = call(*head, *tail, ws)
+        ws = _new((r,), torch.uint8, cache.device, stream)
+        r = call(*args, ws)
     if r:
         raise L.MtpError(-r, where)
+    if stream is not None:
+        _used_on(stream, cache.device, *cache.tensors(), *(t for t in (*head, *tail, ws) if isinstance(t, torch.Tensor)))
     return ws
 
 
-def _head(cache: BlockCache, x, block_table, seq_lens, q_lens, dev_err, stream) -> tuple:
+def _call(cache: BlockCache, x, block_table, seq_lens, q_lens, dev_err, stream) -> tuple:
+    """What every call over a cache begins with."""
     return (C.addressof(cache.desc), cache.device, x, block_table, seq_lens, q_lens, dev_err,
             _address(stream))
 
@@ -390,10 +409,11 @@ def block_append(cache: BlockCache, k, v, block_table, seq_lens, q_lens=None, de
                  stream=None):
     """Writes the new rows k, v [B, T, nkv, hd] (bf16, slices of a projection allowed) at the end
     of each sequence (seq_lens counts them already) and updates scales and means."""
-    r = _block().append(C.addressof(cache.desc), cache.device, k, block_table, seq_lens, q_lens,
-                        dev_err, _address(stream), v)
+    r = _block().append(*_call(cache, k, block_table, seq_lens, q_lens, dev_err, stream), v)
     if r:
         raise L.MtpError(-r, "mtp_block_append")
+    if stream is not None:
+        _used_on(stream, cache.device, *cache.tensors(), k, v, block_table, seq_lens, q_lens, dev_err)
 
 
 def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=None, out=None,
@@ -402,9 +422,8 @@ def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=N
     tokens); out_mass [B, n_table] accumulates each block's softmax weight. Returns (out, ws); a
     ws that is passed in again saves its allocation."""
     out = _new(q.shape, torch.bfloat16, cache.device, stream) if out is None else out
-    ws = _with_ws("mtp_block_attn", _block().attn,
-                  _head(cache, q, block_table, seq_lens, q_lens, dev_err, stream),
-                  (scale, out, out_lse, mass, out_mass), ws, cache.device, stream)
+    ws = _with_ws("mtp_block_attn", _block().attn, cache, (q, block_table, seq_lens, q_lens, dev_err),
+                  (scale, out, out_lse, mass, out_mass), ws, stream)
     return out, ws
 
 
@@ -414,9 +433,8 @@ def block_select(cache: BlockCache, q, block_table, seq_lens, n_sel, n_first=1, 
     query heads with the blocks' mean keys: (sel [B, T, nkv, n_sel] i32, ws)."""
     if out is None:
         out = _new((*q.shape[:2], cache.desc.nkv, n_sel), torch.int32, cache.device, stream)
-    ws = _with_ws("mtp_block_select", _block().select,
-                  _head(cache, q, block_table, seq_lens, q_lens, dev_err, stream),
-                  (n_sel, n_first, n_last, out), ws, cache.device, stream)
+    ws = _with_ws("mtp_block_select", _block().select, cache, (q, block_table, seq_lens, q_lens, dev_err),
+                  (n_sel, n_first, n_last, out), ws, stream)
     return out, ws
 
 
@@ -424,9 +442,8 @@ def block_sparse_attn(cache: BlockCache, q, block_table, seq_lens, sel, q_lens=N
                       out=None, out_lse=None, ws=None, dev_err=None, stream=None):
     """block_attn over the blocks that sel [B, T, nkv, n_sel] lists. Returns (out, ws)."""
     out = _new(q.shape, torch.bfloat16, cache.device, stream) if out is None else out
-    ws = _with_ws("mtp_block_sparse_attn", _block().sparse_attn,
-                  _head(cache, q, block_table, seq_lens, q_lens, dev_err, stream),
-                  (sel, scale, out, out_lse), ws, cache.device, stream)
+    ws = _with_ws("mtp_block_sparse_attn", _block().sparse_attn, cache, (q, block_table, seq_lens, q_lens, dev_err),
+                  (sel, scale, out, out_lse), ws, stream)
     return out, ws
 
 
@@ -445,6 +462,7 @@ def block_evict(block_table, seq_lens, mass, block_size, keep, n_first=1, n_last
                        out_lens, out_mass, freed, n_freed, _address(stream))
     if r:
         raise L.MtpError(-r, "mtp_block_evict")
+    _used_on(stream, dev, block_table, seq_lens, mass, out_table, out_lens, out_mass, freed, n_freed)
     return out_table, out_lens, out_mass, freed, n_freed
 
 
