@@ -264,7 +264,7 @@ def _need(device: int, dtype, numel: int, *tensors):
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)  # (desc holds the tensors' addresses: another tensor is another cache)
 class BlockCache:
     """A block-scaled paged cache: E4M3 codes k, v with logical shape [num_blocks, nkv,
     block_size, hd] (uint8, any strides with hd contiguous), fp32 scales [num_blocks, nkv] and,
@@ -284,15 +284,16 @@ class BlockCache:
 
     def __post_init__(self):
         nb, nkv, bs, hd = self.k.shape
-        self.device = self.k.get_device()
+        object.__setattr__(self, "device", self.k.get_device())
         if self.k.dtype is not torch.uint8 or self.v.dtype is not torch.uint8 or self.v.shape != self.k.shape:
             raise ValueError("k and v: uint8 codes of one shape")
         if self.k.stride() != self.v.stride() or self.k.stride(3) != 1 or self.v.get_device() != self.device:
             raise ValueError("k and v: one layout with hd contiguous, on one device")
         _need(self.device, torch.float32, nb * nkv, self.k_scale, self.v_scale, self.k_mean_scale)
         _need(self.device, torch.int8, nb * nkv * hd, self.k_mean)
-        self.desc = L.mtp_block_cache(nkv, hd, bs, 0, nb, self.k.stride(0), self.k.stride(1),
-                                      self.k.stride(2), *(L._ptr(t) for t in self.tensors()))
+        object.__setattr__(self, "desc", L.mtp_block_cache(
+            nkv, hd, bs, 0, nb, self.k.stride(0), self.k.stride(1), self.k.stride(2),
+            *(L._ptr(t) for t in self.tensors())))
 
     def tensors(self):
         return self.k, self.v, self.k_scale, self.v_scale, self.k_mean, self.k_mean_scale
