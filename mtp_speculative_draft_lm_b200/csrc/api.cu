@@ -397,7 +397,7 @@ mtp_status check_block_cache(const mtp_block_cache* c, bool with_codes, bool wit
         return MTP_ERR_UNSUPPORTED;
     // strides that a tensor copy's 40-bit fields hold, with room for 64-bit byte offsets
     if (with_codes && (c->block_stride >= (int64_t)1 << 39 || c->head_stride >= (int64_t)1 << 39 ||
-                       c->row_stride >= (int64_t)1 << 39 || c->num_blocks * (c->block_stride >> 4) >= (int64_t)1 << 56))
+                       c->row_stride >= (int64_t)1 << 39 || c->block_stride >> 4 >= ((int64_t)1 << 56) / c->num_blocks))
         return MTP_ERR_UNSUPPORTED;
     return MTP_OK;
 }
