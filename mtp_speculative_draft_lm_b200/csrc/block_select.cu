@@ -21,6 +21,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "block_cache.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -418,10 +420,11 @@ cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const 
     const int64_t rows = (int64_t)t.B * t.T * c.nkv;
     if (rows > INT32_MAX) return cudaErrorInvalidValue;
     // a CTA's blocks: as many as leave about four CTAs per SM, at most kMostRounds rounds of its warps
+    // (more only where the grid has no room for that many parts)
     const int64_t rounds = t.n_table * t.B * c.nkv / ((int64_t)kPartBlocks * 148 * 4);
-    p.part = kPartBlocks * (int)(rounds < 1 ? 1 : rounds > kMostRounds ? kMostRounds : rounds);
+    const int64_t least = (t.n_table + (int64_t)kPartBlocks * 65535 - 1) / ((int64_t)kPartBlocks * 65535);
+    p.part = kPartBlocks * (int)std::max(std::min(std::max<int64_t>(rounds, 1), (int64_t)kMostRounds), least);
     const int64_t parts = (t.n_table + p.part - 1) / p.part;
-    if (parts > 65535) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)c.nkv, (unsigned)parts, (unsigned)t.B);
     cudaError_t e = c.hd == 64 ? launch_after(block_score_kernel<64>, grid, kScThreads, 0, s, p)
                   : c.hd == 128 ? launch_after(block_score_kernel<128>, grid, kScThreads, 0, s, p)
