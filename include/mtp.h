@@ -508,7 +508,7 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
  *            buffer; mass without out_mass is MTP_ERR_INVALID_ARG)
  *   ws       (device) >= mtp_block_attn_ws_bytes(cache, B, T, nq, n_table, with_mass) bytes,
  *            16-byte aligned, no initial contents; with_mass = out_mass != NULL
- * Requires nq % nkv == 0, nq / nkv <= 16, 1 <= T <= 64, scale >= 0, and fewer than 2^31 tiles of
+ * Requires nq % nkv == 0, nq / nkv <= 16, 1 <= T <= 64, scale >= 0, B T nq < 2^31, and fewer than 2^31 tiles of
  * 16 positions (and 12 more per unit) over all units: sequences at n_table blocks each, kv heads
  * and groups of at least 8 of a head's T nq / nkv query rows (MTP_ERR_UNSUPPORTED otherwise). Results do not depend on
  * the order in which blocks of the grid run: the same call gives the same bits. */
@@ -532,7 +532,8 @@ mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64
  *   sel      (device) i32 [B, T, nkv, n_sel]: the chosen logical blocks ascending, then -1
  *   ws       (device) >= mtp_block_select_ws_bytes(cache, B, T, n_table) bytes, 16-byte aligned
  * The cache's k and v are not read and may be NULL here; its means are required. n_first >= 0,
- * n_last >= 1, n_first + n_last <= n_sel (MTP_ERR_INVALID_ARG); q, nq and T as mtp_block_attn. */
+ * n_last >= 1, n_first + n_last <= n_sel (MTP_ERR_INVALID_ARG); B T nkv < 2^31; q, nq and T as
+ * mtp_block_attn. */
 size_t mtp_block_select_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
                                  int64_t n_table);
 mtp_status mtp_block_select(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,

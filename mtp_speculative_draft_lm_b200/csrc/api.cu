@@ -454,6 +454,7 @@ mtp_status block_attn_impl(const mtp_block_cache* cache, const uint16_t* q, int6
         if ((int64_t)n_sel * cache->block_size > (int64_t)1 << 30) return MTP_ERR_UNSUPPORTED;
     }
     const mtp::BlockCache c = to_cache(cache);
+    if (!mtp::block_attn_fits(c, B, T, nq, n_table, sparse, n_sel)) return MTP_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 16) ||
         ws_bytes < mtp::block_attn_ws_bytes(c, B, T, nq, n_table, sparse, out_mass != nullptr))
         return MTP_ERR_WORKSPACE;
@@ -484,7 +485,9 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
 size_t mtp_block_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T, int32_t nq,
                                int64_t n_table, int32_t with_mass) {
     if (!sized(cache, B, T, n_table) || !grouped(cache, nq)) return 0;
-    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, n_table, false, with_mass != 0);
+    const mtp::BlockCache c = to_cache(cache);
+    if (!mtp::block_attn_fits(c, B, T, nq, n_table, false, 0)) return 0;
+    return mtp::block_attn_ws_bytes(c, B, T, nq, n_table, false, with_mass != 0);
 }
 
 mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,
@@ -500,7 +503,9 @@ mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64
 size_t mtp_block_sparse_attn_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
                                       int32_t nq, int32_t n_sel) {
     if (!sized(cache, B, T, n_sel) || !grouped(cache, nq)) return 0;
-    return mtp::block_attn_ws_bytes(to_cache(cache), B, T, nq, 1, true, false);
+    const mtp::BlockCache c = to_cache(cache);
+    if (!mtp::block_attn_fits(c, B, T, nq, 1, true, n_sel)) return 0;
+    return mtp::block_attn_ws_bytes(c, B, T, nq, 1, true, false);
 }
 
 mtp_status mtp_block_sparse_attn(const mtp_block_cache* cache, const uint16_t* q,
@@ -517,7 +522,8 @@ mtp_status mtp_block_sparse_attn(const mtp_block_cache* cache, const uint16_t* q
 size_t mtp_block_select_ws_bytes(const mtp_block_cache* cache, int32_t B, int32_t T,
                                  int64_t n_table) {
     if (!sized(cache, B, T, n_table)) return 0;
-    return mtp::block_select_ws_bytes(to_cache(cache), B, T, n_table);
+    const mtp::BlockCache c = to_cache(cache);
+    return mtp::block_select_fits(c, B, T) ? mtp::block_select_ws_bytes(c, B, T, n_table) : 0;
 }
 
 mtp_status mtp_block_select(const mtp_block_cache* cache, const uint16_t* q, int64_t q_stride,
@@ -533,6 +539,7 @@ mtp_status mtp_block_select(const mtp_block_cache* cache, const uint16_t* q, int
     if (!sel || !aligned(sel, 4) || n_first < 0 || n_last < 1 || (int64_t)n_first + n_last > n_sel)
         return MTP_ERR_INVALID_ARG;
     const mtp::BlockCache c = to_cache(cache);
+    if (!mtp::block_select_fits(c, B, T)) return MTP_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 16) || ws_bytes < mtp::block_select_ws_bytes(c, B, T, n_table))
         return MTP_ERR_WORKSPACE;
     const mtp::BlockBatch t{B, T, seq_lens, q_lens, block_table, n_table, dev_err};

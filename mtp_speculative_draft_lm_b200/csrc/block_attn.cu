@@ -1208,6 +1208,12 @@ cudaError_t launch_attn_hd(int nt, const AttnParams& p, const CUtensorMap& km, c
 int block_attn_max_group() { return kMaxGroup; }
 int block_attn_max_t() { return kMaxT; }
 
+bool block_attn_fits(const BlockCache& c, int B, int T, int nq, int64_t n_table, bool sparse, int n_sel) {
+    const Layout l = layout_of(c, B, T, nq, n_table, sparse, false);
+    const int64_t tiles = sparse ? (int64_t)n_sel * (c.bs / 16) : l.tiles;  // (at most 2^26, and units below 2^35)
+    return (int64_t)B * T * nq <= INT32_MAX && l.units * (tiles + kUnitCost) <= INT32_MAX;
+}
+
 size_t block_attn_ws_bytes(const BlockCache& c, int B, int T, int nq, int64_t n_table, bool sparse, bool mass) {
     return layout_of(c, B, T, nq, n_table, sparse, mass).bytes;
 }
@@ -1216,10 +1222,7 @@ cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const Bl
                               cudaStream_t s) {
     const bool sparse = a.sel != nullptr;
     const Layout l = layout_of(c, t.B, t.T, a.nq, t.n_table, sparse, a.out_mass != nullptr);
-    if ((int64_t)t.B * t.T * a.nq > INT32_MAX) return cudaErrorInvalidValue;
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    // tiles of all units on one line: 32-bit indices
-    if ((double)l.units * (double)((sparse ? (int64_t)a.n_sel * (c.bs / 16) : l.tiles) + kUnitCost) >= 2147483648.0) return cudaErrorInvalidValue;
     AttnParams p{c, t, a, 0, a.nq / c.nkv, l.row_tiles, l.tiles, reinterpret_cast<int32_t*>(ws),
                  reinterpret_cast<int32_t*>(ws + l.base), c.bs == 16 ? 0 : c.bs == 32 ? 1 : 2,
                  ((1u << 20) + (uint32_t)(a.nq / c.nkv) - 1u) / (uint32_t)(a.nq / c.nkv), reinterpret_cast<float*>(ws + l.parts),

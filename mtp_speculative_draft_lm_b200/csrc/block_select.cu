@@ -409,6 +409,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) block_evict_kernel(co
 
 }  // namespace
 
+bool block_select_fits(const BlockCache& c, int B, int T) { return (int64_t)B * T * c.nkv <= INT32_MAX; }
+
 size_t block_select_ws_bytes(const BlockCache& c, int B, int T, int64_t n_table) {
     return (((size_t)B * T * c.nkv * n_table * sizeof(uint32_t)) + 15) & ~(size_t)15;
 }
@@ -418,7 +420,6 @@ cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const 
                                 int32_t* sel, void* ws, cudaStream_t s) {
     SelectParams p{c, t, q, q_stride, nq / c.nkv, n_sel, n_first, n_last, sel, static_cast<uint32_t*>(ws), 0};
     const int64_t rows = (int64_t)t.B * t.T * c.nkv;
-    if (rows > INT32_MAX) return cudaErrorInvalidValue;
     // a CTA's blocks: as many as leave about four CTAs per SM, at most kMostRounds rounds of its warps
     // (more only where the grid has no room for that many parts)
     const int64_t rounds = t.n_table * t.B * c.nkv / ((int64_t)kPartBlocks * 148 * 4);

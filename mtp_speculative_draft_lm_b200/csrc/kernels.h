@@ -202,10 +202,13 @@ struct BlockAttnArgs {
 };
 int block_attn_max_group();
 int block_attn_max_t();
+// Whether a call's rows and its line of units have 32-bit indices (n_sel: sparse ones').
+bool block_attn_fits(const BlockCache& c, int B, int T, int nq, int64_t n_table, bool sparse, int n_sel);
 size_t block_attn_ws_bytes(const BlockCache& c, int B, int T, int nq, int64_t n_table, bool sparse,
                            bool mass);
 cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const BlockAttnArgs& a,
                               cudaStream_t s);
+bool block_select_fits(const BlockCache& c, int B, int T);
 size_t block_select_ws_bytes(const BlockCache& c, int B, int T, int64_t n_table);
 cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const uint16_t* q,
                                 int64_t q_stride, int nq, int n_sel, int n_first, int n_last,
