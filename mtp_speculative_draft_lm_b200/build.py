@@ -1,10 +1,13 @@
 """Builds the CUDA library ``libmtp.so`` in-tree for sm_100a (nvcc cross-compiles
 without a GPU). Each ``csrc/*.cu`` becomes an object, rebuilt only when it or a
-header changed; the objects are linked with the static CUDA runtime. Beside it,
-``_block.so``, the module that makes the block cache's calls from torch tensors."""
+header changed; the objects are linked with the static CUDA runtime. Beside it, where
+there is a torch, ``_block.so``, the module that makes the block cache's calls from torch
+tensors: the library itself needs neither torch nor Python's headers."""
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -17,6 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmtp.so")
 CALLS_SRC = os.path.join(CSRC, "block_calls.cpp")
 CALLS = os.path.join(PKG, "_block.so")
+CALLS_KEY = os.path.join(BUILD, "block_calls.key")  # the torch and Python that CALLS was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -45,10 +49,27 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _calls_key() -> str | None:
+    """What _block.so is built for, found without importing torch; None where there is no torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"torch {version} at {os.path.dirname(spec.origin)}, Python {sys.version}"
+
+
 def _build_calls(force: bool) -> None:
-    newest = max(os.path.getmtime(f) for f in [CALLS_SRC, os.path.join(ROOT, "include", "mtp.h")])
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+    key = _calls_key()
+    if key is None:
         return
+    newest = max(os.path.getmtime(f) for f in [CALLS_SRC, os.path.join(ROOT, "include", "mtp.h")])
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest and os.path.exists(CALLS_KEY):
+        with open(CALLS_KEY) as f:
+            if f.read() == key:
+                return
     import sysconfig
 
     import torch
@@ -66,6 +87,20 @@ def _build_calls(force: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS_KEY + f".tmp{os.getpid()}", "w") as f:
+        f.write(key)
+    os.replace(f.name, CALLS_KEY)
+
+
+def _link(objs: list[str]) -> None:
+    if os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs):
+        return
+    tmp = LIB + f".tmp{os.getpid()}"
+    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, LIB)
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -77,15 +112,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
         calls = ex.submit(_build_calls, force)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        calls.result()
-    if os.path.exists(LIB) and os.path.getmtime(LIB) >= max(os.path.getmtime(o) for o in objs):
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        _link(objs)
+        calls.result()  # (raises what went wrong with it: the library is there by now)
     return LIB
 
 
