@@ -182,9 +182,8 @@ PyObject* py_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         Args a{args};
         const Call c(a);
         const at::Tensor* v = a.tensor();
-        if (!v || v->scalar_type() != c.x->scalar_type() || v->sizes() != c.x->sizes() || v->strides() != c.x->strides() ||
-            c.heads != c.cache->nkv || v->get_device() != c.device)
-            throw Refused("k and v must be the cache's heads with one stride, on its device");
+        if (!v || v->sizes() != c.x->sizes() || c.heads != c.cache->nkv || v->get_device() != c.device || token_stride(*v) != c.step)
+            throw Refused("k and v must be the cache's heads with one token stride, on its device");
         const uint16_t *ka = static_cast<const uint16_t*>(c.x->data_ptr()), *va = static_cast<const uint16_t*>(v->data_ptr());
         const Unlocked u;
         return -(int64_t)abi.append(c.cache, ka, va, c.step, (int32_t)c.B, c.T, c.lens, c.q_lens, c.table, c.n_table, c.err, c.stream);
