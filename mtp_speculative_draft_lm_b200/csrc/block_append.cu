@@ -16,7 +16,7 @@
 // in flight before the first is used, and nothing is read twice. The heads of K and V are the
 // fastest grid dimension, so that a row's bytes are read at about the same time. A prompt of
 // 32,768 tokens of 8 heads of 128 takes 41 us (4.9 TB/s; 60% of the issue slots: converting and
-// adding up each code), 24 single tokens 3.4 us, 256 of them 7.4 (13.2 with a CTA to a head, three
+// adding up each code), 24 single tokens 3.5 us, 256 of them 7.4 (13.2 with a CTA to a head, three
 // of its four warps idle).
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -279,17 +279,16 @@ cudaError_t launch_bs(const AppendParams& p, dim3 grid, bool old, cudaStream_t s
 
 template <int HD>
 cudaError_t launch_append(AppendParams p, cudaStream_t s) {
-    // a CTA's block slots: for one head where a step touches as many blocks or leaves SMs idle all
-    // the same, else for several heads (single tokens of 8 heads: 24 sequences 3.4 us, and 3.5 with
-    // four heads to a CTA; 64 sequences 5.4 and 3.7)
+    // a CTA's block slots: for one head as far as a step touches that many blocks, else for several heads
+    // (single tokens of 8 heads of 128 with four heads to a CTA, and with one: 24 sequences 3.5 and 3.7
+    // us, 40 of them 3.5 and 5.2, 24 of 256-wide heads 5.1 and 8.1)
     const int jpc = kAppThreads / 32 / (p.c.bs / 16);
-    const bool few = (int64_t)2 * p.c.nkv * p.t.B <= 4 * 148;
-    while ((1 << p.jt_log) < jpc && (few || (1 << p.jt_log) < p.touch)) ++p.jt_log;
+    while ((1 << p.jt_log) < jpc && (1 << p.jt_log) < p.touch) ++p.jt_log;
     const int jt = 1 << p.jt_log, items = jpc >> p.jt_log;
     const int groups = (p.touch + jt - 1) / jt;
     const dim3 grid((unsigned)((2 * p.c.nkv + items - 1) / items), (unsigned)(groups < 65535 ? groups : 65535), (unsigned)p.t.B);
     // OLD while latency counts, which is while the CTAs fit the SMs at once (us with, without:
-    // 24 single tokens of 8 heads 3.4, 4.1; 256 of them 7.4, 7.7, 512 13.3, 11.9; 64 steps of 16
+    // 24 single tokens of 8 heads 3.5, 4.1; 256 of them 7.4, 7.7, 512 13.3, 11.9; 64 steps of 16
     // tokens 4.4, 5.1, of 64 10.1, 9.3) and most of a step's blocks have earlier rows (16 steps of
     // 64 tokens 4.5, 5.0, of 128 6.1, 5.5; a prompt of 32,768 45.8, 41.4)
     const bool old = p.t.T <= 64 && (int64_t)grid.x * grid.y * grid.z <= 1024;
