@@ -1227,10 +1227,9 @@ cudaError_t block_attn_launch(const BlockCache& c, const BlockBatch& t, const Bl
                  reinterpret_cast<int32_t*>(ws + l.base), c.bs == 16 ? 0 : c.bs == 32 ? 1 : 2,
                  ((1u << 20) + (uint32_t)(a.nq / c.nkv) - 1u) / (uint32_t)(a.nq / c.nkv), reinterpret_cast<float*>(ws + l.parts),
                  reinterpret_cast<float*>(ws + l.row_lse), reinterpret_cast<float*>(ws + l.tile_lse)};
-    int dev = 0, sms = 148;
-    cudaError_t e;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     CUtensorMap km{}, vm{};
     if (!cache_map(&km, c, c.k) || !cache_map(&vm, c, c.v)) return cudaErrorInvalidValue;
     e = c.hd == 64 ? launch_attn_hd<64>(l.nt, p, km, vm, sms, s)

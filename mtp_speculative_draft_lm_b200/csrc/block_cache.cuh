@@ -172,6 +172,13 @@ __device__ __forceinline__ void pick_places(const uint32_t (&k)[KEYS], int n, ui
     }
 }
 
+// SMs of the current device.
+inline cudaError_t sm_count(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 // Lets `kern` use `bytes` of shared memory, asked for once per device.
 template <class K>
 cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& devices) {

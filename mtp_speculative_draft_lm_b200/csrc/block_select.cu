@@ -420,16 +420,19 @@ cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const 
                                 int32_t* sel, void* ws, cudaStream_t s) {
     SelectParams p{c, t, q, q_stride, nq / c.nkv, n_sel, n_first, n_last, sel, static_cast<uint32_t*>(ws), 0};
     const int64_t rows = (int64_t)t.B * t.T * c.nkv;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     // a CTA's blocks: as many as leave about four CTAs per SM, at most kMostRounds rounds of its warps
     // (more only where the grid has no room for that many parts)
-    const int64_t rounds = t.n_table * t.B * c.nkv / ((int64_t)kPartBlocks * 148 * 4);
+    const int64_t rounds = t.n_table * t.B * c.nkv / ((int64_t)kPartBlocks * sms * 4);
     const int64_t least = (t.n_table + (int64_t)kPartBlocks * 65535 - 1) / ((int64_t)kPartBlocks * 65535);
     p.part = kPartBlocks * (int)std::max(std::min(std::max<int64_t>(rounds, 1), (int64_t)kMostRounds), least);
     const int64_t parts = (t.n_table + p.part - 1) / p.part;
     const dim3 grid((unsigned)c.nkv, (unsigned)parts, (unsigned)t.B);
-    cudaError_t e = c.hd == 64 ? launch_after(block_score_kernel<64>, grid, kScThreads, 0, s, p)
-                  : c.hd == 128 ? launch_after(block_score_kernel<128>, grid, kScThreads, 0, s, p)
-                                : launch_after(block_score_kernel<256>, grid, kScThreads, 0, s, p);
+    e = c.hd == 64 ? launch_after(block_score_kernel<64>, grid, kScThreads, 0, s, p)
+        : c.hd == 128 ? launch_after(block_score_kernel<128>, grid, kScThreads, 0, s, p)
+                      : launch_after(block_score_kernel<256>, grid, kScThreads, 0, s, p);
     if (e != cudaSuccess) return e;
     const dim3 g2((unsigned)rows);
     // The fewest threads and keys that hold the table. A barrier of 512 threads costs less than one
@@ -437,7 +440,7 @@ cudaError_t block_select_launch(const BlockCache& c, const BlockBatch& t, const 
     // blocks 36.6, and 38.1 with 1,024 threads; 512 rows of 2,048 27.1 and 29.5), and a CTA alone
     // on its SM is faster with more threads (128 rows of 2,048 16.2 and 15.5).
     if (t.n_table <= 512) return launch_after(block_choose_kernel<256, 2, true>, g2, 256, 0, s, p);
-    if (t.n_table <= 2048 && rows <= 2 * 148) return launch_after(block_choose_kernel<1024, 2, true>, g2, 1024, 0, s, p);
+    if (t.n_table <= 2048 && rows <= 2 * sms) return launch_after(block_choose_kernel<1024, 2, true>, g2, 1024, 0, s, p);
     if (t.n_table <= 2048) return launch_after(block_choose_kernel<512, 4, true>, g2, 512, 0, s, p);
     if (t.n_table <= 8192) return launch_after(block_choose_kernel<512, 16, true>, g2, 512, 0, s, p);
     return launch_after(block_choose_kernel<1024, 8, false>, g2, 1024, 0, s, p);
