@@ -424,7 +424,7 @@ mtp_status mtp_paged_decode_attn(const uint16_t* q, int32_t nq, int32_t nkv, int
  * mtp_block_cache describes the cache (host struct; device pointers inside). Code d of head
  * g, row r of block n is k[n * block_stride + g * head_stride + r * row_stride + d] (strides
  * in bytes, the same for v), so both [block, head, row, hd] (one block's rows of one head
- * contiguous: the faster one to read) and mtp_prefill_kv's [block, row, head, hd] are
+ * contiguous: the faster one to read, 199 us against 273 for 32 long sequences) and mtp_prefill_kv's [block, row, head, hd] are
  * described; a cache that mtp_prefill_kv wrote is read with scales all equal to its k_scale
  * and v_scale. dequant = e4m3(code) * scale[n * nkv + g]; a scale is a finite number >= 0.
  * k_mean and k_mean_scale (both or neither) hold each block's mean key per head:
@@ -481,7 +481,8 @@ typedef struct {
  *   k_mean_scale = ms * s / rows (fp32, each operation rounded to nearest).
  *   k, v   (device) bf16 [B, T, nkv, hd], after RoPE; consecutive tokens kv_stride elements
  *          apart (>= nkv * hd: slices of a fused projection), sequences T * kv_stride apart
- * Rows behind seq_len in the last block are left as they were. Blocks that get rows must
+ * Tokens whose position would be negative are not written (and flagged where the sequence has a
+ * position at all). Rows behind seq_len in the last block are left as they were. Blocks that get rows must
  * belong to one sequence alone (two writers of one block leave either's bytes). T >= 1. */
 mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, const uint16_t* v,
                             int64_t kv_stride, int32_t B, int64_t T, const int32_t* seq_lens,
@@ -500,14 +501,16 @@ mtp_status mtp_block_append(const mtp_block_cache* cache, const uint16_t* k, con
  * weight, whichever is more (for v_scales within 2^90 of the sequence's largest; denominator, lse
  * and mass sum them unrounded). A token
  * that sees no readable position gets zeros, lse -inf and no mass. What lies in masked rows (NaN
- * included) changes nothing.
+ * included) changes nothing. sum_p exp(s_p - max s) |v_scale e4m3(V[p])| has to be finite in fp32.
  *   q        (device) bf16 [B, T, nq, hd], consecutive tokens q_stride elements apart
  *            (>= nq * hd), sequences T * q_stride apart
  *   out      (device) bf16 [B, T, nq, hd] contiguous; out_lse f32 [B, T, nq] or NULL
  *   mass     (device) f32 [B, n_table] or NULL; out_mass the same or NULL (both may be one
  *            buffer; mass without out_mass is MTP_ERR_INVALID_ARG)
  *   ws       (device) >= mtp_block_attn_ws_bytes(cache, B, T, nq, n_table, with_mass) bytes,
- *            16-byte aligned, no initial contents; with_mass = out_mass != NULL
+ *            16-byte aligned, no initial contents; with_mass = out_mass != NULL. Block weights
+ *            take 4 B T nq bytes of it for every 16 positions of the table's width, whatever the
+ *            lengths (32 x 64 tokens of 64 heads over 131,072 positions: 4.3 GB)
  * Requires nq % nkv == 0, nq / nkv <= 16, 1 <= T <= 64, scale >= 0, B T nq < 2^31, and fewer than 2^31 tiles of
  * 16 positions (and 12 more per unit) over all units: sequences at n_table blocks each, kv heads
  * and groups of at least 8 of a head's T nq / nkv query rows (MTP_ERR_UNSUPPORTED otherwise). Results do not depend on
@@ -527,8 +530,9 @@ mtp_status mtp_block_attn(const mtp_block_cache* cache, const uint16_t* q, int64
  *   score_j = max over the group's heads of float(q8 . k_mean_j) * (sq * k_mean_scale_j)
  * (whole-number dot products; fp32, each operation rounded to nearest, so the choice is the
  * same everywhere). The first n_first and the last n_last of those blocks are always taken, then
- * the largest scores (of equal ones the lowest j) until n_sel are. A NaN score counts as the
- * lowest, a head with an infinity or NaN in q does not count, a missing block scores lowest.
+ * the largest scores (of equal ones the lowest j) until n_sel are. A head with an infinity or NaN
+ * in q does not count; a missing block, and one for which no head counts, scores -infinity; a NaN
+ * score comes after those. Where there are n_sel blocks or fewer, all are taken, missing ones too.
  *   sel      (device) i32 [B, T, nkv, n_sel]: the chosen logical blocks ascending, then -1
  *   ws       (device) >= mtp_block_select_ws_bytes(cache, B, T, n_table) bytes, 16-byte aligned
  * The cache's k and v are not read and may be NULL here; its means are required. n_first >= 0,

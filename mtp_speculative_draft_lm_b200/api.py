@@ -272,7 +272,9 @@ class BlockCache:
 
     The block_* calls run on the current stream, or on their argument `stream` (a torch stream or
     its address): the caller orders that one behind what writes their inputs and before what
-    reads their outputs; any tensor of the call may be let go as soon as it returns."""
+    reads their outputs; any tensor of the call may be let go as soon as it returns. Token slots
+    that q_lens leaves empty are not written: in an output that a call makes itself (out=None) they
+    hold whatever its memory held."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
@@ -421,7 +423,8 @@ def block_attn(cache: BlockCache, q, block_table, seq_lens, q_lens=None, scale=N
                out_lse=None, mass=None, out_mass=None, ws=None, dev_err=None, stream=None):
     """Attention of q [B, T, nq, hd] over each sequence's cached positions (causal among the T
     tokens); out_mass [B, n_table] accumulates each block's softmax weight. Returns (out, ws); a
-    ws that is passed in again saves its allocation."""
+    ws that is passed in again saves its allocation. (With out_mass it takes 4 B T nq bytes for
+    every 16 positions of block_table's width: mtp_block_attn_ws_bytes tells.)"""
     out = _new(q.shape, torch.bfloat16, cache.device, stream) if out is None else out
     ws = _with_ws("mtp_block_attn", _block().attn, cache, (q, block_table, seq_lens, q_lens, dev_err),
                   (scale, out, out_lse, mass, out_mass), ws, stream)

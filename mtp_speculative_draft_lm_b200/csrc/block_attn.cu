@@ -33,8 +33,8 @@
 // scaled per row by a power of two).
 // Measured (64 query and 8 kv heads of 128): one sequence of 1,000 positions 7.5 us, of 32,768
 // 20 us; 32 of up to 32,768 with block weights 196 us, 5.7 TB/s; listed blocks (24 x 4 tokens, 256
-// each) 111 us, 6.0 TB/s. 31 x 5 tokens over up to 8,191 positions of 4 heads of 64 (five row
-// tiles) take 53 us, bound by the latency of the decoding, exponentials and products at two
+// each) 112 us, 5.9 TB/s. 31 x 5 tokens over up to 8,191 positions of 4 heads of 64 (five row
+// tiles) take 54 us, bound by the latency of the decoding, exponentials and products at two
 // warps per scheduler.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -57,8 +57,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxGrid = 640;                  // CTAs (workspace slots are sized for it)
 // Steps of the line before each unit's first: what its rows, joins and barriers cost (3 us against
-// half a microsecond a step). A verify batch with short sequences took 56 us with none: the CTAs that
-// had the short ones were the last by a third of that (44 us with 12 or 16, 45 with 8, 48 with 32).
+// half a microsecond a step). With none the CTAs that have the short sequences are the last by far.
+// us with 0, 8, 12, 16, 32: 31 x 5 tokens of 32 heads of 64 over up to 8,191 positions 75, 53.7,
+// 54.0, 54.0, 58.5, over up to 2,000 38.9, 27.0, 26.3, 28.1, 30.7, over up to 400 29, 13.9, 14.4,
+// 15.7, 16.4; 64 tokens of 32 heads of 128 over up to 4,096 74, 54.6, 55.1, 55.7, 58.8.
 constexpr int kUnitCost = 12;
 constexpr float kRaise = 8.f;                  // binades a score may exceed the reference by
 constexpr float kLeastLift = 4.f, kMostLift = 128.f;  // v_scale over the accumulators' unit (kRaise and 7 binades: f16)
@@ -121,7 +123,10 @@ template <int HD, int NT>
 struct Shape {
     static constexpr int kTile = 16 * HD;                        // bytes of K (or V) of a tile
     static constexpr int P = HD == 256 ? 1 : 2;                  // tiles per step
-    // of them worked on together, and CTAs per SM: as the accumulators leave registers
+    // of them worked on together, and CTAs per SM: as the accumulators leave registers. (Three of
+    // 64-wide heads spill 40 bytes at two row tiles and 32 at three, and gain all the same: 32 x 1
+    // token over up to 32,768 positions at 16 rows 70 us, 82 with two CTAs, 32 x 3 at 24 rows 83 and
+    // 98. The 32 rows of 128-wide heads spill 224 bytes.)
     static constexpr int kJoint = HD < 256 && NT <= 2 ? P : 1;
     static constexpr int kPerSm = HD == 64 ? (NT <= 3 ? 3 : 2) : HD == 128 ? (NT <= 1 ? 3 : 2) : 2;
     static constexpr int kQPitch = HD + 8;                       // f16 elements

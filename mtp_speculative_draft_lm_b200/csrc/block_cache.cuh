@@ -132,12 +132,12 @@ __device__ __forceinline__ void pick_threshold(const Each& each, uint32_t want, 
 }
 
 // Where each key stands: *taken bit u says whether key u is picked, before[u] how many picked
-// ones come before it in index order. All threads call it; a block barrier lies between the last
-// read of k and the return.
+// ones come before it in index order. All threads call it; block barriers lie between what they
+// read before the call and what they write after it.
 template <int THREADS, int KEYS>
 __device__ __forceinline__ void pick_places(const uint32_t (&k)[KEYS], int n, uint32_t thr, uint32_t need, PickSmem<THREADS>& sm,
                                             uint32_t* taken, uint32_t (&before)[KEYS]) {
-        constexpr int W = THREADS / 32, N = KEYS * W;  // rows of 32 entries, in index order
+    constexpr int W = THREADS / 32, N = KEYS * W;  // rows of 32 entries, in index order
     static_assert(N <= 256, "sm.tot");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t below = (1u << lane) - 1u;

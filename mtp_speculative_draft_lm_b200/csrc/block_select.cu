@@ -11,13 +11,15 @@
 // instructions.) 16 sequences of up to 131,072 positions and two tokens take 27 us, 2.6 TB/s: the
 // loads' latency with 16 warps per SM. Bulk copies of a block's heads at once took 32 (a warp's
 // lanes issue theirs one after the other), a ring of 16-byte copies 48.
-// The choice is one CTA for each token and head, its keys in registers: a search for the last
+// The choice is one CTA for each token and head, its keys in registers (tables of more than 8,192
+// blocks: read again for each digit and for the places): a search for the last
 // chosen key, then one prefix sum that gives every chosen block its place in the ascending list;
 // 256 lists of 256 from up to 8,192 blocks take 10 us, most of it the search's barriers.
 //
 // Eviction: the same choice of the smallest accumulated weights by one CTA per sequence, whose
 // prefix sum moves the table and the weights up, in place where asked (256 sequences of up to
-// 8,192 blocks: 20 us).
+// 8,192 blocks: 20 us). The forms of 1,024 threads are held to 32 registers and spill 28 bytes (all
+// keys in registers) and 100 (keys read again); one CTA per SM with 64 took 21.5 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
