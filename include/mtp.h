@@ -424,7 +424,7 @@ mtp_status mtp_paged_decode_attn(const uint16_t* q, int32_t nq, int32_t nkv, int
  * mtp_block_cache describes the cache (host struct; device pointers inside). Code d of head
  * g, row r of block n is k[n * block_stride + g * head_stride + r * row_stride + d] (strides
  * in bytes, the same for v), so both [block, head, row, hd] (one block's rows of one head
- * contiguous: the faster one to read, 199 us against 273 for 32 long sequences) and mtp_prefill_kv's [block, row, head, hd] are
+ * contiguous: the faster one to read) and mtp_prefill_kv's [block, row, head, hd] are
  * described; a cache that mtp_prefill_kv wrote is read with scales all equal to its k_scale
  * and v_scale. dequant = e4m3(code) * scale[n * nkv + g]; a scale is a finite number >= 0.
  * k_mean and k_mean_scale (both or neither) hold each block's mean key per head:
